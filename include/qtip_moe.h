@@ -397,6 +397,128 @@ qtip_status qtip_expert_matmul(qtip_moe_plan_t plan, int32_t arm, const uint8_t*
                                const void* a_bf16, int32_t n_rows_a, const int32_t* unit_map, int32_t n_units,
                                float* y, void* stream);
 
+/* ---- routing with a gate ----------------------------------------------------------------
+ * Served MoE models choose their experts by more than the k largest logits.  Of a token's E logits
+ *   s_e = 1 / (1 + exp(-l_e))  (QTIP_GATE_SIGMOID)  or  exp(l_e) / sum_i exp(l_i)  (QTIP_GATE_SOFTMAX)
+ *   c_e = s_e + bias[e]        decides the choice only (a bias that balances the experts' load)
+ *   the experts form num_groups groups of E / num_groups consecutive ones; a group's value is the sum
+ *   of its group_top (1 or 2) largest c_e; the top_groups groups of the largest value stay
+ *   of their experts the k largest c_e are chosen, in descending order
+ *   w_j = s of the j-th choice, divided by the k scores' sum if renormalise, times scale
+ * Ties go to the lower index, among groups and among experts.  The choice is that of s_e and c_e in
+ * fp64 (two experts' c_e can lie closer together than fp32 resolves); the weights are within a factor
+ * 1 +- 2^-21 of the exact ones.  An expert whose logit is -inf or NaN, or whose c_e is -inf or NaN, is
+ * never chosen (a bias of -inf takes an expert out); a +inf logit scores 1 (softmax: shared among
+ * the +inf ones).  A slot that no expert is left for holds the id -1 and the weight 0, and its pair
+ * is in no bin: offsets[E] then is less than n k and the places of sorted_pair past it are not
+ * written.  If the chosen scores' sum is 0, renormalised weights are 0. */
+enum { QTIP_GATE_SOFTMAX = 0, QTIP_GATE_SIGMOID = 1 };
+typedef struct qtip_moe_gate {
+  int32_t score;       /* QTIP_GATE_SOFTMAX or QTIP_GATE_SIGMOID */
+  int32_t num_groups;  /* 1..64, a divisor of E (1: no groups) */
+  int32_t top_groups;  /* 1..num_groups; top_groups * E / num_groups >= k */
+  int32_t group_top;   /* 1 or 2 */
+  int32_t renormalise; /* 0 or 1 */
+  float scale;         /* finite */
+  const float* bias;   /* device [E] fp32, 4-byte aligned, or NULL */
+} qtip_moe_gate;
+
+/* Routes and bins n tokens (the outputs of qtip_moe_route) through a gate.  tile_map and n_tiles may
+ * both be NULL.  workspace: qtip_moe_gate_workspace_bytes(plan) bytes, 256-byte aligned, contents
+ * need no initialisation; two calls that may overlap need one each.  Errors as qtip_moe_route; a bad
+ * gate, one of tile_map and n_tiles NULL without the other, a small or misaligned workspace ->
+ * INVALID_ARG.  qtip_moe_gate_workspace_bytes: host only; 0 for a NULL plan. */
+size_t qtip_moe_gate_workspace_bytes(qtip_moe_plan_t plan);
+qtip_status qtip_moe_gate_route(qtip_moe_plan_t plan, const qtip_moe_gate* gate /*host struct*/, const float* logits,
+                                int32_t n_tokens, int32_t* topk_idx, float* topk_w, int32_t* counts,
+                                int32_t* offsets, int32_t* sorted_pair, int32_t* tile_map, int32_t* n_tiles,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* The layer of qtip_moe_forward with its experts and weights chosen by a gate.  A token's left-out
+ * slots add nothing to its output; a token without any expert gets zeros.  Workspace and errors as
+ * qtip_moe_forward; a bad gate -> INVALID_ARG. */
+qtip_status qtip_moe_forward_gated(qtip_moe_plan_t plan, const qtip_moe_weights* w /*host struct of device ptrs*/,
+                                   const qtip_moe_gate* gate /*host struct*/, const void* x_bf16, const float* logits,
+                                   int32_t n_tokens, void* out, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/* ---- MXFP4: 4-bit microscaled values ------------------------------------------------------
+ * A row of `cols` values is ceil(cols / 32) blocks of 32; a block is 16 bytes of e2m1 codes (value 2i
+ * in the low, value 2i + 1 in the high four bits of byte i) and one e8m0 scale byte (2^(byte - 127);
+ * 255: NaN).  A code's low three bits stand for 0, 0.5, 1, 1.5, 2, 3, 4, 6, its high bit for the sign.
+ * The codes of a matrix are row-major [rows][16 blocks] bytes, its scales [rows][blocks] bytes (the
+ * layout of the OCP microscaling format's checkpoints; no other order is needed).
+ *
+ * qtip_mx_quantize: rows of bf16, fp16 or fp32 values to codes and scales, and, where `values` is not
+ * NULL, to the values that those stand for, converted to the source's type, rows of `cols` (exact, but
+ * for values past the type's range, which the nearest rule can make of amax next to the type's largest
+ * number: they become infinities).
+ *   QTIP_MX_SCALE_FLOOR   scale = 2^(floor(log2 amax) - 2), the OCP rule: values over 6 scales are cut to 6
+ *   QTIP_MX_SCALE_NEAREST the same one step larger where amax >= 1.75 x 2^floor(log2 amax): amax stays
+ *                         under 7 scales, so none is cut by more than rounding would move it
+ *   (scale bytes are held to 0 from below: amax under 2^-124 keeps the scale 2^-127, amax = 0 too.)
+ *   Codes are the nearest value of x / scale, a tie the even code, magnitudes over 6 the code of 6; the
+ *   sign is x's.  A block with a NaN or an infinity gets the scale byte 255 and zero codes: it stands
+ *   for 32 NaNs.  The last block of a row counts as filled up with zeros.
+ *   src [rows] rows of cols elements, row_stride >= cols elements apart, aligned to its type; codes and
+ *   values 16-byte aligned.  rows and cols >= 1 (else INVALID_CONFIG), rows x blocks below 2^31.
+ *   Errors: NULL src, codes or scales, a bad type or rule, row_stride < cols, misalignment, too many
+ *   blocks -> INVALID_ARG; else as qtip_moe_route. */
+enum { QTIP_MX_SRC_BF16 = 0, QTIP_MX_SRC_F16 = 1, QTIP_MX_SRC_F32 = 2 };
+enum { QTIP_MX_SCALE_FLOOR = 0, QTIP_MX_SCALE_NEAREST = 1 };
+#define QTIP_MX_BLOCK 32
+qtip_status qtip_mx_quantize(const void* src, int32_t src_type, int32_t rows, int32_t cols, int64_t row_stride,
+                             int32_t scale_rule, uint8_t* codes, uint8_t* scales, void* values, void* stream);
+
+/* out[i][r] = sum_c a[i][c] w[r][c], i < m, r < n, over k inputs: both operands MXFP4, fp32 accumulation on
+ * v_mfma_scale_f32_*_f8f6f4, out [m][n] bf16 or fp32 (out_dtype).  k must be a multiple of 32 (a row that
+ * qtip_mx_quantize filled up has k = 32 x its blocks).  A NaN scale makes the outputs of its row NaN.
+ * codes 16-byte aligned, scales 4-byte aligned, out 16-byte aligned.  m, n, k >= 1 (else
+ * INVALID_CONFIG); m x k and n x k below 2^37, m x n below 2^40.  Errors: NULL, a bad out_dtype, k % 32,
+ * misalignment, sizes past the limits -> INVALID_ARG; else as qtip_moe_route. */
+qtip_status qtip_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int32_t m, const uint8_t* w_codes,
+                           const uint8_t* w_scales, int32_t n, int32_t k, void* out, int32_t out_dtype, void* stream);
+
+/* ---- MXFP4 experts --------------------------------------------------------------------------
+ * The expert matrices in MXFP4, a third format beside the two 2-bit rungs, with MXFP4 activations. */
+typedef struct qtip_mx_weights {
+  const uint8_t* codes_gate;  /* [E][I][H/2] */
+  const uint8_t* scales_gate; /* [E][I][H/32] */
+  const uint8_t* codes_up;    /* [E][I][H/2] */
+  const uint8_t* scales_up;   /* [E][I][H/32] */
+  const uint8_t* codes_down;  /* [E][H][I/2] */
+  const uint8_t* scales_down; /* [E][H][I/32] */
+} qtip_mx_weights;
+
+/* One expert pass over the pairs of a routed batch (qtip_moe_route, qtip_moe_gate_route), rows in pair
+ * order p = t k + j whatever the bins' order:
+ *   QTIP_MX_PASS_GATE_UP  a = x [n][H]:    out[p] = silu(x[t] Wg^T) * (x[t] Wu^T)   [n k][I]
+ *   QTIP_MX_PASS_DOWN     a = h [n k][I]:  out[p] = h[p] Wd^T                       [n k][H]
+ * with expert e's matrices for the pairs sorted_pair[offsets[e]] .. sorted_pair[offsets[e + 1] - 1], fp32
+ * accumulation, out bf16 or fp32 (out_dtype).  Rows of out whose pair is in no bin are not written.
+ * Offsets outside [0, n k] are held to it and pair ids outside [0, n k) skipped, so device-side garbage
+ * cannot reach memory out of bounds.  Only the pass's own weights are read; the others may be NULL.
+ * Codes and out 16-byte aligned, scales 4-byte aligned; the plan gives E, k, H, I and max_tokens; its
+ * rung, arm and variant do not matter.  Errors as qtip_moe_forward; a bad pass or out_dtype ->
+ * INVALID_ARG. */
+enum { QTIP_MX_PASS_GATE_UP = 0, QTIP_MX_PASS_DOWN = 1 };
+qtip_status qtip_mx_expert_matmul(qtip_moe_plan_t plan, int32_t pass, const qtip_mx_weights* w /*host struct*/,
+                                  const uint8_t* a_codes, const uint8_t* a_scales, const int32_t* offsets,
+                                  const int32_t* sorted_pair, int32_t n_tokens, void* out, int32_t out_dtype,
+                                  void* stream);
+
+/* One MoE layer on MXFP4 experts: route (through `gate`, or as qtip_moe_forward where it is NULL), bin,
+ * quantise x, gate+up, quantise h, down, combine.  x is quantised by the nearest rule, h is rounded to
+ * bf16 and quantised by the nearest rule; y = h Wd^T in fp32; out[t] = sum_j w[t,j] y(t, j) in fp32, j
+ * ascending, cast to the plan's out_dtype.  Left-out slots add nothing.  workspace:
+ * qtip_mx_moe_workspace_bytes(plan) bytes, 256-byte aligned, contents need no initialisation.
+ * Errors as qtip_moe_forward; a bad gate -> INVALID_ARG. */
+size_t qtip_mx_moe_workspace_bytes(qtip_moe_plan_t plan);
+qtip_status qtip_mx_moe_forward(qtip_moe_plan_t plan, const qtip_mx_weights* w /*host struct of device ptrs*/,
+                                const qtip_moe_gate* gate /*host struct or NULL*/, const void* x_bf16,
+                                const float* logits, int32_t n_tokens, void* out, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
 /* ---- observability -----------------------------------------------------------------
  * qtip_moe_stats: copies the plan's launch counters (per arm, and per kernel configuration
  * on the GEMV and grouped arms) into *out; qtip_moe_stats_reset zeroes them.  Host only.

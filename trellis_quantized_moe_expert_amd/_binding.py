@@ -38,6 +38,16 @@ QTIP_RUNG_LUT = 1
 QTIP_SMALL_BATCH_FUSED = 0
 QTIP_SMALL_BATCH_SEPARATE = 1
 QTIP_LUT_RUNG_BITS = 9
+QTIP_GATE_SOFTMAX = 0
+QTIP_GATE_SIGMOID = 1
+QTIP_MX_BLOCK = 32
+QTIP_MX_SRC_BF16 = 0
+QTIP_MX_SRC_F16 = 1
+QTIP_MX_SRC_F32 = 2
+QTIP_MX_SCALE_FLOOR = 0
+QTIP_MX_SCALE_NEAREST = 1
+QTIP_MX_PASS_GATE_UP = 0
+QTIP_MX_PASS_DOWN = 1
 
 
 class qtip_moe_desc(ctypes.Structure):
@@ -81,6 +91,17 @@ class qtip_moe_schedule(ctypes.Structure):
                 ("combine_in_down", ctypes.c_int32)]
 
 
+class qtip_moe_gate(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("num_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("bias", ctypes.c_void_p)]
+
+
+class qtip_mx_weights(ctypes.Structure):
+    _fields_ = [("codes_gate", ctypes.c_void_p), ("scales_gate", ctypes.c_void_p), ("codes_up", ctypes.c_void_p),
+                ("scales_up", ctypes.c_void_p), ("codes_down", ctypes.c_void_p), ("scales_down", ctypes.c_void_p)]
+
+
 class QtipError(RuntimeError):
     def __init__(self, fn: str, status: int, detail: str):
         self.status = status
@@ -120,6 +141,17 @@ _SIGS = {
     "qtip_moe_profile_enable": (_I32, [_P, _I32]),
     "qtip_moe_profile_read": (_I32, [_P, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_I32)]),
     "qtip_measure_lut_gather": (_I32, [_I32, _P, ctypes.c_size_t, _P, ctypes.POINTER(ctypes.c_double)]),
+    "qtip_moe_gate_workspace_bytes": (ctypes.c_size_t, [_P]),
+    "qtip_moe_gate_route": (_I32, [_P, ctypes.POINTER(qtip_moe_gate), _P, _I32, _P, _P, _P, _P, _P, _P, _P, _P,
+                                   ctypes.c_size_t, _P]),
+    "qtip_moe_forward_gated": (_I32, [_P, ctypes.POINTER(qtip_moe_weights), ctypes.POINTER(qtip_moe_gate), _P, _P,
+                                      _I32, _P, _P, ctypes.c_size_t, _P]),
+    "qtip_mx_quantize": (_I32, [_P, _I32, _I32, _I32, ctypes.c_int64, _I32, _P, _P, _P, _P]),
+    "qtip_mx_matmul": (_I32, [_P, _P, _I32, _P, _P, _I32, _I32, _P, _I32, _P]),
+    "qtip_mx_expert_matmul": (_I32, [_P, _I32, ctypes.POINTER(qtip_mx_weights), _P, _P, _P, _P, _I32, _P, _I32, _P]),
+    "qtip_mx_moe_workspace_bytes": (ctypes.c_size_t, [_P]),
+    "qtip_mx_moe_forward": (_I32, [_P, ctypes.POINTER(qtip_mx_weights), ctypes.POINTER(qtip_moe_gate), _P, _P, _I32,
+                                   _P, _P, ctypes.c_size_t, _P]),
     "qtip_status_string": (ctypes.c_char_p, [_I32]),
     "qtip_last_error_detail": (ctypes.c_char_p, []),
 }
@@ -359,6 +391,108 @@ def qtip_measure_lut_gather(rounds: int, sink, sink_elems: int, stream=None) -> 
     _check("qtip_measure_lut_gather", lib().qtip_measure_lut_gather(rounds, _ptr(sink), sink_elems, _stream(stream),
                                                                     ctypes.byref(out)))
     return out.value
+
+
+# ---- the gate and MXFP4 -----------------------------------------------------------------------
+def make_gate(score=QTIP_GATE_SOFTMAX, num_groups=1, top_groups=1, group_top=1, renormalise=1, scale=1.0,
+              bias=None) -> qtip_moe_gate:
+    """A gate; it keeps the bias tensor alive."""
+    g = qtip_moe_gate(score, num_groups, top_groups, group_top, renormalise, scale, _ptr(bias))
+    g.keep = bias
+    return g
+
+
+def make_mx_weights(codes_gate=None, scales_gate=None, codes_up=None, scales_up=None, codes_down=None,
+                    scales_down=None) -> qtip_mx_weights:
+    """MXFP4 expert weights; a pass reads only its own.  The struct keeps the tensors alive."""
+    arrays = (codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down)
+    w = qtip_mx_weights(*(_ptr(a) for a in arrays))
+    w.keep = arrays
+    return w
+
+
+def _on_device(fn: str, tensors: dict) -> None:
+    """Refuse tensors that are not whole arrays in the current GPU's memory ({name: (object, bytes)})."""
+    dev = None
+    for name, (obj, size) in tensors.items():
+        if not hasattr(obj, "get_device"):
+            continue
+        if dev is None:
+            import torch
+            dev = torch.cuda.current_device()
+        if obj.get_device() != dev:
+            raise QtipError(fn, QTIP_ERR_INVALID_ARG, f"{name} is not on the current device (cuda:{dev})")
+        if not obj.is_contiguous():
+            raise QtipError(fn, QTIP_ERR_INVALID_ARG, f"{name} must be contiguous")
+        if obj.numel() * obj.element_size() < size:
+            raise QtipError(fn, QTIP_ERR_INVALID_ARG, f"{name} is smaller than {size} bytes")
+
+
+def qtip_moe_gate_workspace_bytes(plan) -> int:
+    return lib().qtip_moe_gate_workspace_bytes(plan)
+
+
+def qtip_moe_gate_route(plan, gate: qtip_moe_gate, logits, n_tokens, topk_idx, topk_w, counts, offsets, sorted_pair,
+                        tile_map, n_tiles, workspace, workspace_bytes, stream=None) -> None:
+    _on_device("qtip_moe_gate_route", {
+        "logits": (logits, 0), "topk_idx": (topk_idx, 0), "topk_w": (topk_w, 0), "counts": (counts, 0),
+        "offsets": (offsets, 0), "sorted_pair": (sorted_pair, 0), "tile_map": (tile_map, 0), "n_tiles": (n_tiles, 4),
+        "workspace": (workspace, workspace_bytes), "bias": (getattr(gate, "keep", None), 0)})
+    _check("qtip_moe_gate_route", lib().qtip_moe_gate_route(
+        plan, ctypes.byref(gate), _ptr(logits), n_tokens, _ptr(topk_idx), _ptr(topk_w), _ptr(counts), _ptr(offsets),
+        _ptr(sorted_pair), _ptr(tile_map), _ptr(n_tiles), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def qtip_moe_forward_gated(plan, weights: qtip_moe_weights, gate: qtip_moe_gate, x_bf16, logits, n_tokens, out,
+                           workspace, workspace_bytes, stream=None) -> None:
+    _on_device("qtip_moe_forward_gated", {
+        "x_bf16": (x_bf16, 0), "logits": (logits, 0), "out": (out, 0), "workspace": (workspace, workspace_bytes),
+        "bias": (getattr(gate, "keep", None), 0)})
+    _check("qtip_moe_forward_gated", lib().qtip_moe_forward_gated(
+        plan, ctypes.byref(weights), ctypes.byref(gate), _ptr(x_bf16), _ptr(logits), n_tokens, _ptr(out),
+        _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def qtip_mx_quantize(src, src_type, rows, cols, row_stride, scale_rule, codes, scales, values=None,
+                     stream=None) -> None:
+    blocks = (cols + QTIP_MX_BLOCK - 1) // QTIP_MX_BLOCK
+    size = 4 if src_type == QTIP_MX_SRC_F32 else 2
+    _on_device("qtip_mx_quantize", {"codes": (codes, rows * blocks * 16), "scales": (scales, rows * blocks),
+                                    "values": (values, rows * cols * size)})
+    _check("qtip_mx_quantize", lib().qtip_mx_quantize(_ptr(src), src_type, rows, cols, row_stride, scale_rule,
+                                                      _ptr(codes), _ptr(scales), _ptr(values), _stream(stream)))
+
+
+def qtip_mx_matmul(a_codes, a_scales, m, w_codes, w_scales, n, k, out, out_dtype, stream=None) -> None:
+    _on_device("qtip_mx_matmul", {
+        "a_codes": (a_codes, m * k // 2), "a_scales": (a_scales, m * k // 32), "w_codes": (w_codes, n * k // 2),
+        "w_scales": (w_scales, n * k // 32), "out": (out, m * n * (4 if out_dtype == QTIP_OUT_F32 else 2))})
+    _check("qtip_mx_matmul", lib().qtip_mx_matmul(_ptr(a_codes), _ptr(a_scales), m, _ptr(w_codes), _ptr(w_scales), n,
+                                                  k, _ptr(out), out_dtype, _stream(stream)))
+
+
+def qtip_mx_expert_matmul(plan, pass_, weights: qtip_mx_weights, a_codes, a_scales, offsets, sorted_pair, n_tokens,
+                          out, out_dtype, stream=None) -> None:
+    _on_device("qtip_mx_expert_matmul", {
+        "a_codes": (a_codes, 0), "a_scales": (a_scales, 0), "offsets": (offsets, 0), "sorted_pair": (sorted_pair, 0),
+        "out": (out, 0)})
+    _check("qtip_mx_expert_matmul", lib().qtip_mx_expert_matmul(
+        plan, pass_, ctypes.byref(weights), _ptr(a_codes), _ptr(a_scales), _ptr(offsets), _ptr(sorted_pair), n_tokens,
+        _ptr(out), out_dtype, _stream(stream)))
+
+
+def qtip_mx_moe_workspace_bytes(plan) -> int:
+    return lib().qtip_mx_moe_workspace_bytes(plan)
+
+
+def qtip_mx_moe_forward(plan, weights: qtip_mx_weights, gate, x_bf16, logits, n_tokens, out, workspace,
+                        workspace_bytes, stream=None) -> None:
+    _on_device("qtip_mx_moe_forward", {
+        "x_bf16": (x_bf16, 0), "logits": (logits, 0), "out": (out, 0), "workspace": (workspace, workspace_bytes),
+        "bias": (getattr(gate, "keep", None), 0)})
+    _check("qtip_mx_moe_forward", lib().qtip_mx_moe_forward(
+        plan, ctypes.byref(weights), None if gate is None else ctypes.byref(gate), _ptr(x_bf16), _ptr(logits),
+        n_tokens, _ptr(out), _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def raw_status(fn_name: str, *args) -> int:

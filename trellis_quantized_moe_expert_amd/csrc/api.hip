@@ -8,6 +8,7 @@
 // witness declines under graph capture and caches only a successful answer.  The variant
 // knob follows the prefill page (PR #196): an unknown value warns and keeps the default.
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
@@ -17,6 +18,7 @@
 
 #include "../../include/qtip_moe.h"
 #include "fill_predicate.h"
+#include "mx_internal.h"
 #include "qtip_internal.h"
 
 using namespace qtip;
@@ -738,13 +740,50 @@ qtip_status qtip_expert_matmul(qtip_moe_plan_t plan, int32_t arm, const uint8_t*
 
 namespace {
 
+qtip_status check_gate(const qtip_moe_plan_s* plan, const qtip_moe_gate* g) {
+  if (!g) return fail(QTIP_ERR_INVALID_ARG, "gate is NULL");
+  const int32_t E = plan->d.num_experts;
+  if (g->score != QTIP_GATE_SOFTMAX && g->score != QTIP_GATE_SIGMOID)
+    return fail(QTIP_ERR_INVALID_ARG, "gate: score must be QTIP_GATE_SOFTMAX or QTIP_GATE_SIGMOID");
+  if (g->num_groups < 1 || g->num_groups > kGateMaxGroups || E % g->num_groups)
+    return fail(QTIP_ERR_INVALID_ARG, "gate: num_groups must be in [1, 64] and divide num_experts");
+  if (g->top_groups < 1 || g->top_groups > g->num_groups)
+    return fail(QTIP_ERR_INVALID_ARG, "gate: top_groups must be in [1, num_groups]");
+  if (g->top_groups * (E / g->num_groups) < plan->d.top_k)
+    return fail(QTIP_ERR_INVALID_ARG, "gate: the kept groups hold fewer than top_k experts");
+  if (g->group_top != 1 && g->group_top != 2) return fail(QTIP_ERR_INVALID_ARG, "gate: group_top must be 1 or 2");
+  if (g->renormalise != 0 && g->renormalise != 1) return fail(QTIP_ERR_INVALID_ARG, "gate: renormalise must be 0 or 1");
+  if (!std::isfinite(g->scale)) return fail(QTIP_ERR_INVALID_ARG, "gate: scale must be finite");
+  if (reinterpret_cast<uintptr_t>(g->bias) & 3) return fail(QTIP_ERR_INVALID_ARG, "gate: bias must be 4-byte aligned");
+  return QTIP_OK;
+}
+
+GateParams gate_params(const qtip_moe_plan_s* plan, const qtip_moe_gate* g, const float* logits, int32_t n,
+                       int32_t* topk_idx, float* topk_w) {
+  GateParams p{};
+  p.logits = logits;
+  p.bias = g->bias;
+  p.n = n;
+  p.E = plan->d.num_experts;
+  p.k = plan->d.top_k;
+  p.sigmoid = g->score == QTIP_GATE_SIGMOID;
+  p.groups = g->num_groups;
+  p.top_groups = g->top_groups;
+  p.group_top = g->group_top;
+  p.renormalise = g->renormalise;
+  p.scale = g->scale;
+  p.topk_idx = topk_idx;
+  p.topk_w = topk_w;
+  return p;
+}
+
 // The layer from router logits (logits != NULL) or from hidden states through the router
 // GEMM (w_router != NULL; its K-chunk partial sums go to the workspace and the top-k kernel
-// adds them).  The workspace regions are laid out for the plan's max_tokens, or, with
+// adds them), the experts chosen by a gate where one is given (already checked).  The workspace regions are laid out for the plan's max_tokens, or, with
 // layout_for_n (the allocation-free entry point), for this call's n_tokens only.
 qtip_status forward_impl(qtip_moe_plan_t plan, const qtip_moe_weights* w, const void* x_bf16, const float* logits,
                          const void* w_router, int32_t n_tokens, void* out, void* workspace, size_t workspace_bytes,
-                         void* stream, bool layout_for_n = false) {
+                         void* stream, bool layout_for_n = false, const qtip_moe_gate* gate = nullptr) {
   g_detail.clear();
   if (!plan || !w || !x_bf16 || !(logits || w_router) || !out || !workspace)
     return fail(QTIP_ERR_INVALID_ARG, "NULL argument");
@@ -766,7 +805,8 @@ qtip_status forward_impl(qtip_moe_plan_t plan, const qtip_moe_weights* w, const 
   if (s != QTIP_OK) return s;
 
   const qtip_moe_desc& d = plan->d;
-  const CallChoice choice = call_choice(plan, n_tokens);
+  CallChoice choice = call_choice(plan, n_tokens);
+  if (gate) choice.route_in_gate_up = false;  // that launch knows the plain routing only
   const int32_t arm = choice.arm;
   const int karm = choice.karm;
   if (karm == kArmDense && !plan->dense) return fail(QTIP_ERR_INVALID_CONFIG, "the plan has no dequantize workspace");
@@ -840,6 +880,14 @@ qtip_status forward_impl(qtip_moe_plan_t plan, const qtip_moe_weights* w, const 
   if (choice.route_in_gate_up) {
     // routed and binned inside the gate/up launch below (the "route" stage is empty)
     if ((e = prof_mark(plan, 1, st)) != hipSuccess) return hip_fail(e, "profile event");
+  } else if (gate) {
+    e = launch_gate(gate_params(plan, gate, lg, n_tokens, topk_idx, topk_w), st);
+    if (e != hipSuccess) return hip_fail(e, "gate launch");
+    if ((e = prof_mark(plan, 1, st)) != hipSuccess) return hip_fail(e, "profile event");
+    e = launch_bin(topk_idx, P, d.num_experts, plan->tile_m, counts, offsets, sorted_pair, tile_map, n_tiles,
+                   frag ? padded_pair : nullptr, frag ? n_pad : nullptr, &um, st);
+    if (e != hipSuccess) return hip_fail(e, "bin launch");
+    plan->stats.route_launches += 2;
   } else if (n_tokens <= kFusedRouteMaxTokens) {
     // one workgroup routes and bins a small batch (the "route" stage then holds both)
     e = launch_route_bin(lg, n_part, n_tokens, d.num_experts, d.top_k, topk_idx, topk_w, plan->tile_m, counts, offsets,
@@ -993,7 +1041,8 @@ qtip_status forward_impl(qtip_moe_plan_t plan, const qtip_moe_weights* w, const 
   if (pp.tok_split) {
     plan->stats.combined_in_down++;  // the "combine" stage is empty
   } else {
-    e = launch_combine(y, topk_w, n_tokens, d.top_k, d.hidden, out, d.out_dtype == QTIP_OUT_BF16, st);
+    e = launch_combine(y, topk_w, n_tokens, d.top_k, d.hidden, out, d.out_dtype == QTIP_OUT_BF16, st,
+                       gate ? topk_idx : nullptr, d.num_experts);
     if (e != hipSuccess) return hip_fail(e, "combine launch");
     plan->stats.combine_launches++;
   }
@@ -1004,6 +1053,79 @@ qtip_status forward_impl(qtip_moe_plan_t plan, const qtip_moe_weights* w, const 
   plan->stats.last_arm = arm;
   plan->stats.last_n_tokens = n_tokens;
   return QTIP_OK;
+}
+
+// The current device, for entry points without a plan.
+qtip_status ensure_current(hipStream_t stream, int* dev_out) {
+  const qtip_status s = current_device(dev_out);
+  return s == QTIP_OK ? witness_on(*dev_out, stream) : s;
+}
+
+// ---- MXFP4 experts ----------------------------------------------------------------------------
+bool mx_aligned(const void* codes, const void* scales) {
+  return !(reinterpret_cast<uintptr_t>(codes) & 15) && !(reinterpret_cast<uintptr_t>(scales) & 3);
+}
+
+qtip_status check_mx_pass(int32_t pass, const qtip_mx_weights* w) {
+  if (pass != QTIP_MX_PASS_GATE_UP && pass != QTIP_MX_PASS_DOWN) return fail(QTIP_ERR_INVALID_ARG, "unknown pass");
+  const bool gu = pass == QTIP_MX_PASS_GATE_UP;
+  const void* codes[2] = {gu ? w->codes_gate : w->codes_down, gu ? w->codes_up : w->codes_down};
+  const void* scales[2] = {gu ? w->scales_gate : w->scales_down, gu ? w->scales_up : w->scales_down};
+  for (int i = 0; i < 2; ++i) {
+    if (!codes[i] || !scales[i]) return fail(QTIP_ERR_INVALID_ARG, "NULL weight pointer");
+    if (!mx_aligned(codes[i], scales[i]))
+      return fail(QTIP_ERR_INVALID_ARG, "weight codes must be 16-byte aligned, scales 4-byte aligned");
+  }
+  return QTIP_OK;
+}
+
+MxMatmulParams mx_pass_params(const qtip_moe_plan_s* plan, int32_t pass, const qtip_mx_weights* w,
+                              const uint8_t* a_codes, const uint8_t* a_scales, const int32_t* offsets,
+                              const int32_t* sorted_pair, int32_t n_tokens, void* out, int32_t out_dtype) {
+  const bool gu = pass == QTIP_MX_PASS_GATE_UP;
+  MxMatmulParams p{};
+  p.a = a_codes;
+  p.a_scale = a_scales;
+  p.w0 = gu ? w->codes_gate : w->codes_down;
+  p.w0_scale = gu ? w->scales_gate : w->scales_down;
+  p.w1 = gu ? w->codes_up : nullptr;
+  p.w1_scale = gu ? w->scales_up : nullptr;
+  p.offsets = offsets;
+  p.sorted_pair = sorted_pair;
+  p.E = plan->d.num_experts;
+  p.a_div = gu ? plan->d.top_k : 1;
+  p.m = n_tokens * plan->d.top_k;
+  p.n = gu ? plan->d.inter : plan->d.hidden;
+  p.blocks = (gu ? plan->d.hidden : plan->d.inter) / kMxBlock;
+  p.out = out;
+  p.out_bf16 = out_dtype == QTIP_OUT_BF16;
+  return p;
+}
+
+struct MxWsLayout {
+  size_t topk_idx, topk_w, counts, offsets, sorted_pair, tile_map, n_tiles, x_codes, x_scales, h_codes, h_scales, y,
+      total;
+};
+
+MxWsLayout mx_ws_layout(const qtip_moe_desc& d) {
+  const size_t n = d.max_tokens, P = n * d.top_k;
+  const size_t wide = d.hidden > d.inter ? d.hidden : d.inter;  // y [P][H] fp32; before it, h [P][I] bf16
+  MxWsLayout L{};
+  size_t o = 0;
+  L.topk_idx = o;     o = align256(o + P * 4);
+  L.topk_w = o;       o = align256(o + P * 4);
+  L.counts = o;       o = align256(o + (size_t)d.num_experts * 4);
+  L.offsets = o;      o = align256(o + ((size_t)d.num_experts + 1) * 4);
+  L.sorted_pair = o;  o = align256(o + P * 4);
+  L.tile_map = o;     o = align256(o + P * 12);
+  L.n_tiles = o;      o = align256(o + 4);
+  L.x_codes = o;      o = align256(o + n * d.hidden / 2);
+  L.x_scales = o;     o = align256(o + n * d.hidden / kMxBlock);
+  L.h_codes = o;      o = align256(o + P * d.inter / 2);
+  L.h_scales = o;     o = align256(o + P * d.inter / kMxBlock);
+  L.y = o;            o = align256(o + P * wide * 4);
+  L.total = o;
+  return L;
 }
 
 }  // namespace
@@ -1241,6 +1363,230 @@ qtip_status qtip_moe_log_engaged(qtip_moe_plan_t plan, int32_t n_tokens, int32_t
   std::fprintf(stderr, "%s\n", line);
   std::fflush(stderr);
   if (printed) *printed = 1;
+  return QTIP_OK;
+}
+
+// ---- the gate ---------------------------------------------------------------------------------
+
+size_t qtip_moe_gate_workspace_bytes(qtip_moe_plan_t plan) {
+  if (!plan) return 0;
+  return align256((size_t)plan->d.max_tokens * plan->d.top_k * 12) + 256;
+}
+
+qtip_status qtip_moe_gate_route(qtip_moe_plan_t plan, const qtip_moe_gate* gate, const float* logits,
+                                int32_t n_tokens, int32_t* topk_idx, float* topk_w, int32_t* counts,
+                                int32_t* offsets, int32_t* sorted_pair, int32_t* tile_map, int32_t* n_tiles,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  g_detail.clear();
+  if (!plan || !logits || !topk_idx || !topk_w || !counts || !offsets || !sorted_pair || !workspace)
+    return fail(QTIP_ERR_INVALID_ARG, "NULL argument");
+  if (!tile_map != !n_tiles) return fail(QTIP_ERR_INVALID_ARG, "tile_map and n_tiles must both be given or both be NULL");
+  qtip_status s = check_gate(plan, gate);
+  if (s != QTIP_OK) return s;
+  if (n_tokens <= 0 || n_tokens > plan->d.max_tokens)
+    return fail(QTIP_ERR_INVALID_CONFIG, "n_tokens must be in [1, max_tokens]");
+  if (workspace_bytes < qtip_moe_gate_workspace_bytes(plan) || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return fail(QTIP_ERR_INVALID_ARG, "workspace too small or not 256-byte aligned");
+  const hipStream_t st = (hipStream_t)stream;
+  int dev = 0;
+  if ((s = ensure_device(plan, st, &dev)) != QTIP_OK) return s;
+  const qtip_moe_desc& d = plan->d;
+  if (!tile_map) {
+    tile_map = reinterpret_cast<int32_t*>(workspace);
+    n_tiles = tile_map + (size_t)d.max_tokens * d.top_k * 3;
+  }
+  hipError_t e = launch_gate(gate_params(plan, gate, logits, n_tokens, topk_idx, topk_w), st);
+  if (e != hipSuccess) return hip_fail(e, "gate launch");
+  plan->stats.route_launches++;
+  e = launch_bin(topk_idx, n_tokens * d.top_k, d.num_experts, plan->tile_m, counts, offsets, sorted_pair, tile_map,
+                 n_tiles, nullptr, nullptr, nullptr, st);
+  if (e != hipSuccess) return hip_fail(e, "bin launch");
+  plan->stats.route_launches++;
+  return QTIP_OK;
+}
+
+qtip_status qtip_moe_forward_gated(qtip_moe_plan_t plan, const qtip_moe_weights* w, const qtip_moe_gate* gate,
+                                   const void* x_bf16, const float* logits, int32_t n_tokens, void* out,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  g_detail.clear();
+  if (!plan || !logits) return fail(QTIP_ERR_INVALID_ARG, "NULL argument");
+  const qtip_status s = check_gate(plan, gate);
+  if (s != QTIP_OK) return s;
+  return forward_impl(plan, w, x_bf16, logits, nullptr, n_tokens, out, workspace, workspace_bytes, stream, false, gate);
+}
+
+// ---- MXFP4 ------------------------------------------------------------------------------------
+
+qtip_status qtip_mx_quantize(const void* src, int32_t src_type, int32_t rows, int32_t cols, int64_t row_stride,
+                             int32_t scale_rule, uint8_t* codes, uint8_t* scales, void* values, void* stream) {
+  g_detail.clear();
+  if (!src || !codes || !scales) return fail(QTIP_ERR_INVALID_ARG, "NULL argument");
+  if (src_type != QTIP_MX_SRC_BF16 && src_type != QTIP_MX_SRC_F16 && src_type != QTIP_MX_SRC_F32)
+    return fail(QTIP_ERR_INVALID_ARG, "unknown src_type");
+  if (scale_rule != QTIP_MX_SCALE_FLOOR && scale_rule != QTIP_MX_SCALE_NEAREST)
+    return fail(QTIP_ERR_INVALID_ARG, "unknown scale_rule");
+  if (rows < 1 || cols < 1) return fail(QTIP_ERR_INVALID_CONFIG, "rows and cols must be >= 1 (an empty launch is an error)");
+  if (row_stride < cols) return fail(QTIP_ERR_INVALID_ARG, "row_stride must be at least cols");
+  if ((int64_t)rows * (((int64_t)cols + kMxBlock - 1) / kMxBlock) >= ((int64_t)1 << 31))
+    return fail(QTIP_ERR_INVALID_ARG, "rows * blocks must be below 2^31");
+  if (row_stride >= ((int64_t)1 << 40)) return fail(QTIP_ERR_INVALID_ARG, "row_stride must be below 2^40");
+  if ((reinterpret_cast<uintptr_t>(src) & (src_type == QTIP_MX_SRC_F32 ? 3 : 1)) ||
+      (reinterpret_cast<uintptr_t>(codes) & 15) || (reinterpret_cast<uintptr_t>(values) & 15))
+    return fail(QTIP_ERR_INVALID_ARG, "src must be aligned to its type, codes and values to 16 bytes");
+  const hipStream_t st = (hipStream_t)stream;
+  int dev = 0;
+  const qtip_status s = ensure_current(st, &dev);
+  if (s != QTIP_OK) return s;
+  MxQuantParams p{};
+  p.src = src;
+  p.row_stride = row_stride;
+  p.rows = rows;
+  p.cols = cols;
+  p.source = src_type;
+  p.nearest = scale_rule == QTIP_MX_SCALE_NEAREST;
+  p.codes = codes;
+  p.scales = scales;
+  p.values = values;
+  const hipError_t e = launch_mx_quantize(p, st);
+  return e == hipSuccess ? QTIP_OK : hip_fail(e, "MXFP4 quantize launch");
+}
+
+qtip_status qtip_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int32_t m, const uint8_t* w_codes,
+                           const uint8_t* w_scales, int32_t n, int32_t k, void* out, int32_t out_dtype, void* stream) {
+  g_detail.clear();
+  if (!a_codes || !a_scales || !w_codes || !w_scales || !out) return fail(QTIP_ERR_INVALID_ARG, "NULL argument");
+  if (out_dtype != QTIP_OUT_BF16 && out_dtype != QTIP_OUT_F32) return fail(QTIP_ERR_INVALID_ARG, "unknown out_dtype");
+  if (m < 1 || n < 1 || k < 1) return fail(QTIP_ERR_INVALID_CONFIG, "m, n and k must be >= 1 (an empty launch is an error)");
+  if (k % kMxBlock) return fail(QTIP_ERR_INVALID_ARG, "k must be a multiple of 32");
+  if ((int64_t)m * k >= ((int64_t)1 << 37) || (int64_t)n * k >= ((int64_t)1 << 37) ||
+      (int64_t)m * n >= ((int64_t)1 << 40))
+    return fail(QTIP_ERR_INVALID_ARG, "m * k and n * k must be below 2^37, m * n below 2^40");
+  if (!mx_aligned(a_codes, a_scales) || !mx_aligned(w_codes, w_scales) || (reinterpret_cast<uintptr_t>(out) & 15))
+    return fail(QTIP_ERR_INVALID_ARG, "codes and out must be 16-byte aligned, scales 4-byte aligned");
+  const hipStream_t st = (hipStream_t)stream;
+  int dev = 0;
+  const qtip_status s = ensure_current(st, &dev);
+  if (s != QTIP_OK) return s;
+  MxMatmulParams p{};
+  p.a = a_codes;
+  p.a_scale = a_scales;
+  p.w0 = w_codes;
+  p.w0_scale = w_scales;
+  p.E = 1;
+  p.a_div = 1;
+  p.m = m;
+  p.n = n;
+  p.blocks = k / kMxBlock;
+  p.out = out;
+  p.out_bf16 = out_dtype == QTIP_OUT_BF16;
+  const hipError_t e = launch_mx_matmul(p, st);
+  return e == hipSuccess ? QTIP_OK : hip_fail(e, "MXFP4 matmul launch");
+}
+
+qtip_status qtip_mx_expert_matmul(qtip_moe_plan_t plan, int32_t pass, const qtip_mx_weights* w,
+                                  const uint8_t* a_codes, const uint8_t* a_scales, const int32_t* offsets,
+                                  const int32_t* sorted_pair, int32_t n_tokens, void* out, int32_t out_dtype,
+                                  void* stream) {
+  g_detail.clear();
+  if (!plan || !w || !a_codes || !a_scales || !offsets || !sorted_pair || !out)
+    return fail(QTIP_ERR_INVALID_ARG, "NULL argument");
+  qtip_status s = check_mx_pass(pass, w);
+  if (s != QTIP_OK) return s;
+  if (out_dtype != QTIP_OUT_BF16 && out_dtype != QTIP_OUT_F32) return fail(QTIP_ERR_INVALID_ARG, "unknown out_dtype");
+  if (!mx_aligned(a_codes, a_scales) || (reinterpret_cast<uintptr_t>(out) & 15))
+    return fail(QTIP_ERR_INVALID_ARG, "codes and out must be 16-byte aligned, scales 4-byte aligned");
+  if (n_tokens <= 0 || n_tokens > plan->d.max_tokens)
+    return fail(QTIP_ERR_INVALID_CONFIG, "n_tokens must be in [1, max_tokens] (an empty launch is an error)");
+  const hipStream_t st = (hipStream_t)stream;
+  int dev = 0;
+  if ((s = ensure_device(plan, st, &dev)) != QTIP_OK) return s;
+  const hipError_t e = launch_mx_matmul(
+      mx_pass_params(plan, pass, w, a_codes, a_scales, offsets, sorted_pair, n_tokens, out, out_dtype), st);
+  return e == hipSuccess ? QTIP_OK : hip_fail(e, "MXFP4 expert launch");
+}
+
+size_t qtip_mx_moe_workspace_bytes(qtip_moe_plan_t plan) { return plan ? mx_ws_layout(plan->d).total : 0; }
+
+qtip_status qtip_mx_moe_forward(qtip_moe_plan_t plan, const qtip_mx_weights* w, const qtip_moe_gate* gate,
+                                const void* x_bf16, const float* logits, int32_t n_tokens, void* out, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  g_detail.clear();
+  if (!plan || !w || !x_bf16 || !logits || !out || !workspace) return fail(QTIP_ERR_INVALID_ARG, "NULL argument");
+  qtip_status s;
+  if ((s = check_mx_pass(QTIP_MX_PASS_GATE_UP, w)) != QTIP_OK) return s;
+  if ((s = check_mx_pass(QTIP_MX_PASS_DOWN, w)) != QTIP_OK) return s;
+  if (gate && (s = check_gate(plan, gate)) != QTIP_OK) return s;
+  if ((reinterpret_cast<uintptr_t>(x_bf16) & 15) || (reinterpret_cast<uintptr_t>(out) & 15))
+    return fail(QTIP_ERR_INVALID_ARG, "x and out must be 16-byte aligned");
+  if (n_tokens <= 0 || n_tokens > plan->d.max_tokens)
+    return fail(QTIP_ERR_INVALID_CONFIG, "n_tokens must be in [1, max_tokens] (an empty launch is an error)");
+  const qtip_moe_desc& d = plan->d;
+  const MxWsLayout L = mx_ws_layout(d);
+  if (workspace_bytes < L.total || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return fail(QTIP_ERR_INVALID_ARG, "workspace too small or not 256-byte aligned");
+  const hipStream_t st = (hipStream_t)stream;
+  int dev = 0;
+  if ((s = ensure_device(plan, st, &dev)) != QTIP_OK) return s;
+  char* ws = reinterpret_cast<char*>(workspace);
+  int32_t* topk_idx = reinterpret_cast<int32_t*>(ws + L.topk_idx);
+  float* topk_w = reinterpret_cast<float*>(ws + L.topk_w);
+  int32_t* counts = reinterpret_cast<int32_t*>(ws + L.counts);
+  int32_t* offsets = reinterpret_cast<int32_t*>(ws + L.offsets);
+  int32_t* sorted_pair = reinterpret_cast<int32_t*>(ws + L.sorted_pair);
+  int32_t* tile_map = reinterpret_cast<int32_t*>(ws + L.tile_map);
+  int32_t* n_tiles = reinterpret_cast<int32_t*>(ws + L.n_tiles);
+  uint8_t* x_codes = reinterpret_cast<uint8_t*>(ws + L.x_codes);
+  uint8_t* x_scales = reinterpret_cast<uint8_t*>(ws + L.x_scales);
+  uint8_t* h_codes = reinterpret_cast<uint8_t*>(ws + L.h_codes);
+  uint8_t* h_scales = reinterpret_cast<uint8_t*>(ws + L.h_scales);
+  float* y = reinterpret_cast<float*>(ws + L.y);
+  const int32_t P = n_tokens * d.top_k;
+
+  hipError_t e;
+  if (!gate && n_tokens <= kFusedRouteMaxTokens) {
+    e = launch_route_bin(logits, 1, n_tokens, d.num_experts, d.top_k, topk_idx, topk_w, plan->tile_m, counts, offsets,
+                         sorted_pair, tile_map, n_tiles, nullptr, nullptr, nullptr, st);
+    if (e != hipSuccess) return hip_fail(e, "route/bin launch");
+    plan->stats.route_launches++;
+  } else {
+    e = gate ? launch_gate(gate_params(plan, gate, logits, n_tokens, topk_idx, topk_w), st)
+             : launch_route_topk(logits, 1, n_tokens, d.num_experts, d.top_k, topk_idx, topk_w, st);
+    if (e != hipSuccess) return hip_fail(e, "routing launch");
+    e = launch_bin(topk_idx, P, d.num_experts, plan->tile_m, counts, offsets, sorted_pair, tile_map, n_tiles, nullptr,
+                   nullptr, nullptr, st);
+    if (e != hipSuccess) return hip_fail(e, "bin launch");
+    plan->stats.route_launches += 2;
+  }
+  MxQuantParams q{};
+  q.src = x_bf16;
+  q.row_stride = d.hidden;
+  q.rows = n_tokens;
+  q.cols = d.hidden;
+  q.source = kMxBf16;
+  q.nearest = 1;
+  q.codes = x_codes;
+  q.scales = x_scales;
+  e = launch_mx_quantize(q, st);
+  if (e != hipSuccess) return hip_fail(e, "MXFP4 quantize launch");
+  // h takes the place of y: it is read for the last time before the down pass writes y
+  e = launch_mx_matmul(mx_pass_params(plan, QTIP_MX_PASS_GATE_UP, w, x_codes, x_scales, offsets, sorted_pair, n_tokens,
+                                      y, QTIP_OUT_BF16), st);
+  if (e != hipSuccess) return hip_fail(e, "MXFP4 gate/up launch");
+  q.src = y;
+  q.row_stride = d.inter;
+  q.rows = P;
+  q.cols = d.inter;
+  q.codes = h_codes;
+  q.scales = h_scales;
+  e = launch_mx_quantize(q, st);  // rows of left-out pairs hold anything; no later launch reads them
+  if (e != hipSuccess) return hip_fail(e, "MXFP4 quantize launch");
+  e = launch_mx_matmul(mx_pass_params(plan, QTIP_MX_PASS_DOWN, w, h_codes, h_scales, offsets, sorted_pair, n_tokens, y,
+                                      QTIP_OUT_F32), st);
+  if (e != hipSuccess) return hip_fail(e, "MXFP4 down launch");
+  e = launch_combine(y, topk_w, n_tokens, d.top_k, d.hidden, out, d.out_dtype == QTIP_OUT_BF16, st, topk_idx,
+                     d.num_experts);
+  if (e != hipSuccess) return hip_fail(e, "combine launch");
+  plan->stats.combine_launches++;
   return QTIP_OK;
 }
 
