@@ -113,7 +113,8 @@ def check_product(a, w, kind):
 
 SIZES = [(1, 1, 32), (1, 16, 64), (1, 4096, 512), (2, 17, 96), (3, 100, 544), (15, 33, 1056), (16, 16, 2048),
          (17, 64, 512), (33, 48, 4096), (64, 130, 640), (65, 128, 128), (100, 257, 416), (128, 256, 256),
-         (129, 72, 992), (255, 300, 1024), (256, 256, 4096), (300, 513, 160), (513, 1040, 2080), (1, 24, 8192)]
+         (129, 72, 992), (255, 300, 1024), (256, 256, 4096), (300, 513, 160), (513, 1040, 2080), (1, 24, 8192),
+         (40, 50, 96), (20, 70, 32), (700, 300, 128), (520, 264, 1184)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp32"])
