@@ -191,10 +191,18 @@ def _ptr(obj):
     return int(obj)
 
 
+try:  # torch's own way to the current stream's handle: 0.4 us against 3.6 through the stream object
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+except ImportError:
+    _raw_stream = None
+
+
 def _stream(stream):
     if stream is None:
         try:
             import torch
+            if _raw_stream is not None and torch.cuda.is_initialized():
+                return _raw_stream(torch.cuda.current_device())
             if torch.cuda.is_available():
                 return torch.cuda.current_stream().cuda_stream
         except ImportError:
@@ -411,20 +419,24 @@ def make_mx_weights(codes_gate=None, scales_gate=None, codes_up=None, scales_up=
     return w
 
 
-def _on_device(fn: str, tensors: dict) -> None:
-    """Refuse tensors that are not whole arrays in the current GPU's memory ({name: (object, bytes)})."""
-    dev = None
-    for name, (obj, size) in tensors.items():
-        if not hasattr(obj, "get_device"):
+def _on_device(fn: str, *items) -> None:
+    """Refuse tensors that are not whole arrays in the current GPU's memory: (name, object, bytes)s."""
+    dev = -1
+    for name, obj, size in items:
+        if obj is None or obj.__class__ is int:
             continue
-        if dev is None:
+        try:
+            where, whole, nbytes = obj.get_device(), obj.is_contiguous(), obj.nbytes
+        except AttributeError:  # an address holder other than a torch tensor
+            continue
+        if dev < 0:
             import torch
             dev = torch.cuda.current_device()
-        if obj.get_device() != dev:
+        if where != dev:
             raise QtipError(fn, QTIP_ERR_INVALID_ARG, f"{name} is not on the current device (cuda:{dev})")
-        if not obj.is_contiguous():
+        if not whole:
             raise QtipError(fn, QTIP_ERR_INVALID_ARG, f"{name} must be contiguous")
-        if obj.numel() * obj.element_size() < size:
+        if nbytes < size:
             raise QtipError(fn, QTIP_ERR_INVALID_ARG, f"{name} is smaller than {size} bytes")
 
 
@@ -434,10 +446,10 @@ def qtip_moe_gate_workspace_bytes(plan) -> int:
 
 def qtip_moe_gate_route(plan, gate: qtip_moe_gate, logits, n_tokens, topk_idx, topk_w, counts, offsets, sorted_pair,
                         tile_map, n_tiles, workspace, workspace_bytes, stream=None) -> None:
-    _on_device("qtip_moe_gate_route", {
-        "logits": (logits, 0), "topk_idx": (topk_idx, 0), "topk_w": (topk_w, 0), "counts": (counts, 0),
-        "offsets": (offsets, 0), "sorted_pair": (sorted_pair, 0), "tile_map": (tile_map, 0), "n_tiles": (n_tiles, 4),
-        "workspace": (workspace, workspace_bytes), "bias": (getattr(gate, "keep", None), 0)})
+    _on_device("qtip_moe_gate_route", ("logits", logits, 0), ("topk_idx", topk_idx, 0), ("topk_w", topk_w, 0),
+               ("counts", counts, 0), ("offsets", offsets, 0), ("sorted_pair", sorted_pair, 0),
+               ("tile_map", tile_map, 0), ("n_tiles", n_tiles, 4), ("workspace", workspace, workspace_bytes),
+               ("bias", getattr(gate, "keep", None), 0))
     _check("qtip_moe_gate_route", lib().qtip_moe_gate_route(
         plan, ctypes.byref(gate), _ptr(logits), n_tokens, _ptr(topk_idx), _ptr(topk_w), _ptr(counts), _ptr(offsets),
         _ptr(sorted_pair), _ptr(tile_map), _ptr(n_tiles), _ptr(workspace), workspace_bytes, _stream(stream)))
@@ -445,9 +457,8 @@ def qtip_moe_gate_route(plan, gate: qtip_moe_gate, logits, n_tokens, topk_idx, t
 
 def qtip_moe_forward_gated(plan, weights: qtip_moe_weights, gate: qtip_moe_gate, x_bf16, logits, n_tokens, out,
                            workspace, workspace_bytes, stream=None) -> None:
-    _on_device("qtip_moe_forward_gated", {
-        "x_bf16": (x_bf16, 0), "logits": (logits, 0), "out": (out, 0), "workspace": (workspace, workspace_bytes),
-        "bias": (getattr(gate, "keep", None), 0)})
+    _on_device("qtip_moe_forward_gated", ("x_bf16", x_bf16, 0), ("logits", logits, 0), ("out", out, 0),
+               ("workspace", workspace, workspace_bytes), ("bias", getattr(gate, "keep", None), 0))
     _check("qtip_moe_forward_gated", lib().qtip_moe_forward_gated(
         plan, ctypes.byref(weights), ctypes.byref(gate), _ptr(x_bf16), _ptr(logits), n_tokens, _ptr(out),
         _ptr(workspace), workspace_bytes, _stream(stream)))
@@ -457,25 +468,24 @@ def qtip_mx_quantize(src, src_type, rows, cols, row_stride, scale_rule, codes, s
                      stream=None) -> None:
     blocks = (cols + QTIP_MX_BLOCK - 1) // QTIP_MX_BLOCK
     size = 4 if src_type == QTIP_MX_SRC_F32 else 2
-    _on_device("qtip_mx_quantize", {"codes": (codes, rows * blocks * 16), "scales": (scales, rows * blocks),
-                                    "values": (values, rows * cols * size)})
+    _on_device("qtip_mx_quantize", ("codes", codes, rows * blocks * 16), ("scales", scales, rows * blocks),
+               ("values", values, rows * cols * size))
     _check("qtip_mx_quantize", lib().qtip_mx_quantize(_ptr(src), src_type, rows, cols, row_stride, scale_rule,
                                                       _ptr(codes), _ptr(scales), _ptr(values), _stream(stream)))
 
 
 def qtip_mx_matmul(a_codes, a_scales, m, w_codes, w_scales, n, k, out, out_dtype, stream=None) -> None:
-    _on_device("qtip_mx_matmul", {
-        "a_codes": (a_codes, m * k // 2), "a_scales": (a_scales, m * k // 32), "w_codes": (w_codes, n * k // 2),
-        "w_scales": (w_scales, n * k // 32), "out": (out, m * n * (4 if out_dtype == QTIP_OUT_F32 else 2))})
+    _on_device("qtip_mx_matmul", ("a_codes", a_codes, m * k // 2), ("a_scales", a_scales, m * k // 32),
+               ("w_codes", w_codes, n * k // 2), ("w_scales", w_scales, n * k // 32),
+               ("out", out, m * n * (4 if out_dtype == QTIP_OUT_F32 else 2)))
     _check("qtip_mx_matmul", lib().qtip_mx_matmul(_ptr(a_codes), _ptr(a_scales), m, _ptr(w_codes), _ptr(w_scales), n,
                                                   k, _ptr(out), out_dtype, _stream(stream)))
 
 
 def qtip_mx_expert_matmul(plan, pass_, weights: qtip_mx_weights, a_codes, a_scales, offsets, sorted_pair, n_tokens,
                           out, out_dtype, stream=None) -> None:
-    _on_device("qtip_mx_expert_matmul", {
-        "a_codes": (a_codes, 0), "a_scales": (a_scales, 0), "offsets": (offsets, 0), "sorted_pair": (sorted_pair, 0),
-        "out": (out, 0)})
+    _on_device("qtip_mx_expert_matmul", ("a_codes", a_codes, 0), ("a_scales", a_scales, 0), ("offsets", offsets, 0),
+               ("sorted_pair", sorted_pair, 0), ("out", out, 0))
     _check("qtip_mx_expert_matmul", lib().qtip_mx_expert_matmul(
         plan, pass_, ctypes.byref(weights), _ptr(a_codes), _ptr(a_scales), _ptr(offsets), _ptr(sorted_pair), n_tokens,
         _ptr(out), out_dtype, _stream(stream)))
@@ -487,9 +497,8 @@ def qtip_mx_moe_workspace_bytes(plan) -> int:
 
 def qtip_mx_moe_forward(plan, weights: qtip_mx_weights, gate, x_bf16, logits, n_tokens, out, workspace,
                         workspace_bytes, stream=None) -> None:
-    _on_device("qtip_mx_moe_forward", {
-        "x_bf16": (x_bf16, 0), "logits": (logits, 0), "out": (out, 0), "workspace": (workspace, workspace_bytes),
-        "bias": (getattr(gate, "keep", None), 0)})
+    _on_device("qtip_mx_moe_forward", ("x_bf16", x_bf16, 0), ("logits", logits, 0), ("out", out, 0),
+               ("workspace", workspace, workspace_bytes), ("bias", getattr(gate, "keep", None), 0))
     _check("qtip_mx_moe_forward", lib().qtip_mx_moe_forward(
         plan, ctypes.byref(weights), None if gate is None else ctypes.byref(gate), _ptr(x_bf16), _ptr(logits),
         n_tokens, _ptr(out), _ptr(workspace), workspace_bytes, _stream(stream)))

@@ -2,16 +2,15 @@
 // one e8m0 scale.
 //
 //   floor rule:   scale = 2^(floor(log2 amax) - 2)   (2 = the exponent of the largest code, 6)
-//   nearest rule: the same with amax rounded to the nearest power of two's code first: one step
-//                 larger when amax >= 1.75 * 2^floor(log2 amax), so that amax / scale < 7
+//   nearest rule: one step larger when amax >= 1.75 * 2^floor(log2 amax), so that amax / scale < 7
 //   code = the e2m1 value nearest to x / scale (a tie: the even code), at most 6
 //
-// The scale's exponent is read from the bits of amax (no logarithm).  A block that holds a NaN or
-// an infinity gets the scale 255 (NaN) and zero codes: it stands for NaN as a whole.  The last
-// block of a row whose length is no multiple of 32 counts as filled up with zeros.
+// The scale's exponent is read from the bits of amax (no logarithm), and the gfx950 conversions with
+// a scale (v_cvt_scalef32_pk_fp4_*) round two values at a time; they take the scale by the exponent
+// bits of a float, so the byte 0 (2^-127) is the float of those bits.  A block that holds a NaN or an
+// infinity gets the scale 255 (NaN) and zero codes: it stands for NaN as a whole.  The last block of
+// a row whose length is no multiple of 32 counts as filled up with zeros.
 #include "mx_internal.h"
-
-#include <hip/hip_bf16.h>
 
 namespace qtip {
 
@@ -20,84 +19,136 @@ namespace {
 constexpr int kQuantThreads = 256;
 constexpr int kPerThread = 8;  // values of one thread; four neighbouring threads hold a block
 
-// The e2m1 code of x * inv, x finite.  inv is a power of two, in two factors because 2^(127 - byte)
-// alone can leave fp32's range; the products are exact unless they fall below every border.
-__device__ inline uint32_t e2m1_code(float x, float inv0, float inv1) {
-  const float a = fabsf(x) * inv0 * inv1;
-  uint32_t c = 0;
-  c += a > 0.25f;
-  c += a >= 0.75f;
-  c += a > 1.25f;
-  c += a >= 1.75f;
-  c += a > 2.5f;
-  c += a >= 3.5f;
-  c += a > 5.0f;
-  return c | (__builtin_bit_cast(uint32_t, x) >> 28 & 8u);
-}
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
-__device__ inline float e2m1_value(uint32_t c) {
-  const uint32_t m = c & 7u;
-  const float mag = m < 2 ? 0.5f * (float)m : (float)(2u + (m & 1u)) * (float)(1u << (m >> 1)) * 0.25f;
-  return c & 8u ? -mag : mag;
-}
+// What differs between the source types: eight values as dwords, their largest magnitude as the bits
+// of a float (magnitudes order as integers), and the conversions.
+struct Bf16 {
+  typedef uint16_t Elem;
+  static constexpr int kWords = 4;
+  static __device__ uint32_t top(const uint32_t (&w)[4]) {
+    u16x2 m = __builtin_bit_cast(u16x2, w[0] & 0x7fff7fffu);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu));
+    return (uint32_t)max(m[0], m[1]) << 16;
+  }
+  template <int I> static __device__ uint32_t code(uint32_t old, const uint32_t (&w)[4], float scale) {
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, __builtin_bit_cast(bf16x2, w[I]), scale, I);
+  }
+  template <int I> static __device__ void value(uint32_t codes, float scale, uint32_t (&w)[4]) {
+    w[I] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, I));
+  }
+  static constexpr uint32_t kNan = 0x7fc07fc0u;
+};
 
-__device__ inline float pow2(int e) { return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23); }
+struct F16 {
+  typedef uint16_t Elem;
+  static constexpr int kWords = 4;
+  static __device__ uint32_t top(const uint32_t (&w)[4]) {
+    const uint32_t m = Bf16::top(w) >> 16;  // the same integer order
+    return __builtin_bit_cast(uint32_t, (float)__builtin_bit_cast(_Float16, (uint16_t)m));
+  }
+  template <int I> static __device__ uint32_t code(uint32_t old, const uint32_t (&w)[4], float scale) {
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(old, __builtin_bit_cast(f16x2, w[I]), scale, I);
+  }
+  template <int I> static __device__ void value(uint32_t codes, float scale, uint32_t (&w)[4]) {
+    w[I] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, I));
+  }
+  static constexpr uint32_t kNan = 0x7e007e00u;
+};
 
-template <typename T> __device__ inline float load_one(const T* p);
-template <> __device__ inline float load_one<uint16_t>(const uint16_t* p) {
-  return __builtin_bit_cast(float, (uint32_t)*p << 16);
-}
-template <> __device__ inline float load_one<_Float16>(const _Float16* p) { return (float)*p; }
-template <> __device__ inline float load_one<float>(const float* p) { return *p; }
+struct F32 {
+  typedef uint32_t Elem;
+  static constexpr int kWords = 8;
+  static __device__ uint32_t top(const uint32_t (&w)[8]) {
+    uint32_t m = w[0] & 0x7fffffffu;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
+    return m;
+  }
+  template <int I> static __device__ uint32_t code(uint32_t old, const uint32_t (&w)[8], float scale) {
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, __builtin_bit_cast(float, w[2 * I]),
+                                                    __builtin_bit_cast(float, w[2 * I + 1]), scale, I);
+  }
+  template <int I> static __device__ void value(uint32_t codes, float scale, uint32_t (&w)[8]) {
+    const f32x2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, I);
+    const float lo = v[0], hi = v[1];  // a bit cast of a vector's element itself reads element 0
+    w[2 * I] = __builtin_bit_cast(uint32_t, lo);
+    w[2 * I + 1] = __builtin_bit_cast(uint32_t, hi);
+  }
+  static constexpr uint32_t kNan = 0x7fc00000u;
+};
 
-__device__ inline void store_one(uint16_t* p, float v) {  // v is a bf16 value
-  *p = (uint16_t)(__builtin_bit_cast(uint32_t, v) >> 16);
-}
-__device__ inline void store_one(_Float16* p, float v) { *p = (_Float16)v; }
-__device__ inline void store_one(float* p, float v) { *p = v; }
-
-template <typename T>
+template <class T, bool VALUES>
 __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(MxQuantParams p) {
-  const int blocks = (p.cols + kMxBlock - 1) / kMxBlock;
-  const int64_t per_row = (int64_t)blocks * (kMxBlock / kPerThread);
+  typedef typename T::Elem Elem;
+  constexpr int kWords = T::kWords;
+  struct __attribute__((packed, aligned(sizeof(Elem)))) Eight { uint32_t w[kWords]; };  // at any element's address
+  const uint32_t blocks = (uint32_t)(p.cols + kMxBlock - 1) / kMxBlock;
   const int64_t item = (int64_t)blockIdx.x * kQuantThreads + threadIdx.x;
-  if (item >= per_row * p.rows) return;  // a block's four threads leave together
-  const int64_t row = item / per_row;
-  const int part = (int)(item - row * per_row);
+  const uint32_t block = (uint32_t)(item >> 2);  // rows x blocks < 2^31
+  if (block >= blocks * (uint32_t)p.rows) return;  // a block's four threads leave together
+  const uint32_t row = block / blocks;
+  const int part = (int)((block - row * blocks) * 4) + (int)(item & 3);
   const int c0 = part * kPerThread;
-  const T* src = reinterpret_cast<const T*>(p.src) + row * p.row_stride;
-  float v[kPerThread];
-  uint32_t top = 0;
+  const Elem* src = reinterpret_cast<const Elem*>(p.src) + (int64_t)row * p.row_stride + c0;
+  uint32_t w[kWords];
+  if (c0 + kPerThread <= p.cols) {
+    const Eight v = *reinterpret_cast<const Eight*>(src);
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    v[i] = c0 + i < p.cols ? load_one(src + c0 + i) : 0.0f;
-    top = max(top, __builtin_bit_cast(uint32_t, v[i]) & 0x7fffffffu);  // magnitudes order as integers
-  }
-  top = max(top, (uint32_t)__shfl_xor((int)top, 1, 64));
-  top = max(top, (uint32_t)__shfl_xor((int)top, 2, 64));
-  const bool bad = top >= 0x7f800000u;
-  if (p.nearest) top += 0x200000u;
-  const int field = (int)(top >> 23);
-  const int byte = bad ? 255 : max(field - 2, 0);
-  uint32_t packed = 0;
-  const int up = (127 - byte) >> 1;
-  const float inv0 = pow2(up), inv1 = pow2(127 - byte - up);
-  const float s0 = pow2(-up), s1 = pow2(up - (127 - byte));
-  float value[kPerThread];
+    for (int i = 0; i < kWords; ++i) w[i] = v.w[i];
+  } else {
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const uint32_t c = bad ? 0u : e2m1_code(v[i], inv0, inv1);
-    packed |= c << (4 * i);
-    value[i] = bad ? __builtin_nanf("") : e2m1_value(c) * s0 * s1;
-  }
-  *reinterpret_cast<uint32_t*>(p.codes + row * blocks * kMxBlockBytes + part * 4) = packed;
-  if ((part & 3) == 0) p.scales[row * blocks + (part >> 2)] = (uint8_t)byte;
-  if (p.values) {
-    T* dst = reinterpret_cast<T*>(p.values) + row * p.cols;
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i)
-      if (c0 + i < p.cols) store_one(dst + c0 + i, value[i]);
+      if (c0 + i < p.cols) w[i * kWords / 8] |= (uint32_t)src[i] << (kWords == 4 ? 16 * (i & 1) : 0);
   }
+  uint32_t top = T::top(w);
+  top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xF, 0xF, true));  // quad lanes 1 0 3 2
+  top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x4E, 0xF, 0xF, true));  // quad lanes 2 3 0 1
+  const bool bad = top >= 0x7f800000u;
+  if (p.nearest) top += 0x200000u;
+  const uint32_t byte = bad ? 255u : (uint32_t)max((int)(top >> 23) - 2, 0);
+  const float scale = __builtin_bit_cast(float, byte << 23);
+  uint32_t codes = 0;
+  codes = T::template code<0>(codes, w, scale);
+  codes = T::template code<1>(codes, w, scale);
+  codes = T::template code<2>(codes, w, scale);
+  codes = T::template code<3>(codes, w, scale);
+  if (bad) codes = 0;
+  *reinterpret_cast<uint32_t*>(p.codes + (size_t)block * kMxBlockBytes + (item & 3) * 4) = codes;
+  if ((item & 3) == 0) p.scales[block] = (uint8_t)byte;
+  if (VALUES) {
+    Elem* dst = reinterpret_cast<Elem*>(p.values) + (int64_t)row * p.cols + c0;
+    Eight v;
+    T::template value<0>(codes, scale, v.w);
+    T::template value<1>(codes, scale, v.w);
+    T::template value<2>(codes, scale, v.w);
+    T::template value<3>(codes, scale, v.w);
+    if (bad) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) v.w[i] = T::kNan;
+    }
+    if (c0 + kPerThread <= p.cols) {
+      *reinterpret_cast<Eight*>(dst) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i)
+        if (c0 + i < p.cols) dst[i] = (Elem)(v.w[i * kWords / 8] >> (kWords == 4 ? 16 * (i & 1) : 0));
+    }
+  }
+}
+
+template <class T>
+void launch_source(const MxQuantParams& p, dim3 grid, hipStream_t stream) {
+  if (p.values)
+    hipLaunchKernelGGL((quantize_kernel<T, true>), grid, dim3(kQuantThreads), 0, stream, p);
+  else
+    hipLaunchKernelGGL((quantize_kernel<T, false>), grid, dim3(kQuantThreads), 0, stream, p);
 }
 
 }  // namespace
@@ -105,12 +156,9 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(MxQuantParams p
 hipError_t launch_mx_quantize(const MxQuantParams& p, hipStream_t stream) {
   const int64_t items = (int64_t)((p.cols + kMxBlock - 1) / kMxBlock) * (kMxBlock / kPerThread) * p.rows;
   const dim3 grid((unsigned)((items + kQuantThreads - 1) / kQuantThreads));
-  if (p.source == kMxBf16)
-    hipLaunchKernelGGL(quantize_kernel<uint16_t>, grid, dim3(kQuantThreads), 0, stream, p);
-  else if (p.source == kMxF16)
-    hipLaunchKernelGGL(quantize_kernel<_Float16>, grid, dim3(kQuantThreads), 0, stream, p);
-  else
-    hipLaunchKernelGGL(quantize_kernel<float>, grid, dim3(kQuantThreads), 0, stream, p);
+  if (p.source == kMxBf16) launch_source<Bf16>(p, grid, stream);
+  else if (p.source == kMxF16) launch_source<F16>(p, grid, stream);
+  else launch_source<F32>(p, grid, stream);
   return hipGetLastError();
 }
 
