@@ -1095,6 +1095,7 @@ MxMatmulParams mx_pass_params(const qtip_moe_plan_s* plan, int32_t pass, const q
   p.E = plan->d.num_experts;
   p.a_div = gu ? plan->d.top_k : 1;
   p.m = n_tokens * plan->d.top_k;
+  p.a_rows = gu ? n_tokens : p.m;
   p.n = gu ? plan->d.inter : plan->d.hidden;
   p.blocks = (gu ? plan->d.hidden : plan->d.inter) / kMxBlock;
   p.out = out;
@@ -1474,6 +1475,7 @@ qtip_status qtip_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int3
   p.w0_scale = w_scales;
   p.E = 1;
   p.a_div = 1;
+  p.a_rows = m;
   p.m = m;
   p.n = n;
   p.blocks = k / kMxBlock;

@@ -57,8 +57,9 @@ struct MxMatmulParams {
   const uint8_t* w1_scale;
   const int32_t* offsets;      // [E + 1], or NULL: dense rows 0 .. m - 1
   const int32_t* sorted_pair;  // [m]
-  int32_t E;
+  int32_t E;       // matrices in w0 (and w1)
   int32_t a_div;
+  int32_t a_rows;  // rows of a
   int32_t m;       // rows of y: dense rows, or pairs
   int32_t n;       // rows of one w matrix
   int32_t blocks;  // 32-value blocks of a row (K / 32)

@@ -144,14 +144,17 @@ __device__ inline void tile_of_block(const MxMatmulParams& p, int tiles, int row
   rb = in / 8;
 }
 
-constexpr int kDirectWaves = 8;
-
+// ---- the direct kernel ----------------------------------------------------------------------
 // One workgroup: 16 weight rows (of both matrices where there are two) by MB * 16 activation rows;
-// its waves split the inputs, run by run of 512, and add their sums through LDS.
-template <int MB, int HALVES>
-__global__ __launch_bounds__(kDirectWaves * 64) void direct_kernel(MxMatmulParams p) {
-  __shared__ f32x4 red[kDirectWaves][HALVES * MB][64];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+// its W waves split the inputs, run by run of 512, and add their sums through LDS.  Operands go from
+// memory to registers: with few activation rows a call is a stream of weights, and the more of them
+// are asked for at once the better.
+// TAIL: the rows do not end with a run.
+template <int MB, int HALVES, int W, bool TAIL>
+__global__ __launch_bounds__(W * 64, MB * HALVES == 1 ? 6 : MB * HALVES == 2 ? 5 : 2) void direct_kernel(
+    MxMatmulParams p) {
+  __shared__ f32x4 red[W][HALVES * MB][64];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int j = lane & 15, g = lane >> 4;
   const int row_blocks = (p.n + 15) >> 4;
   const int tile = (int)blockIdx.x / row_blocks;
@@ -163,6 +166,37 @@ __global__ __launch_bounds__(kDirectWaves * 64) void direct_kernel(MxMatmulParam
   const size_t wrow = (size_t)expert * p.n + min(n0 + j, p.n - 1);
   const uint8_t* wc[2] = {p.w0 + wrow * row_codes, HALVES == 2 ? p.w1 + wrow * row_codes : nullptr};
   const uint8_t* ws[2] = {p.w0_scale + wrow * p.blocks, HALVES == 2 ? p.w1_scale + wrow * p.blocks : nullptr};
+
+  // Four blocks of a row from block `first` on, and their scales; zero codes past the row's end.
+  auto load = [&](const uint8_t* codes, const uint8_t* scales, int first, i32x4 (&c)[4], int& s) {
+    typedef uint32_t __attribute__((aligned(1))) u32_any;
+    if (!TAIL) {
+#pragma unroll
+      for (int st = 0; st < 4; ++st)
+        c[st] = *reinterpret_cast<const i32x4*>(codes + (size_t)(first + st) * kMxBlockBytes);
+      s = (int)*reinterpret_cast<const u32_any*>(scales + first);
+    } else {
+      s = 0;
+#pragma unroll
+      for (int st = 0; st < 4; ++st) {  // blocks past the end read the last one again; no branches
+        const bool in = first + st < p.blocks;
+        const int at = min(first + st, p.blocks - 1);
+        const i32x4 v = *reinterpret_cast<const i32x4*>(codes + (size_t)at * kMxBlockBytes);
+        const int scale = scales[at];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[st][i] = in ? v[i] : 0;
+        s |= (in ? scale : 127) << (8 * st);
+      }
+    }
+  };
+  int first = wv * 16 + 4 * g;
+  i32x4 w[HALVES][4];
+  int sw[HALVES];
+  if (wv * 16 < p.blocks) {  // before the activation rows are looked up
+#pragma unroll
+    for (int h = 0; h < HALVES; ++h) load(wc[h], ws[h], first, w[h], sw[h]);
+  }
+
   const uint8_t* ac[MB];
   const uint8_t* as[MB];
 #pragma unroll
@@ -178,25 +212,9 @@ __global__ __launch_bounds__(kDirectWaves * 64) void direct_kernel(MxMatmulParam
 #pragma unroll
     for (int b = 0; b < MB; ++b) acc[h][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  auto load = [&](const uint8_t* codes, const uint8_t* scales, int first, i32x4 (&c)[4], int& s) {
-    s = 0;
-#pragma unroll
-    for (int st = 0; st < 4; ++st) {
-      c[st] = i32x4{0, 0, 0, 0};
-      if (first + st < p.blocks) {
-        c[st] = *reinterpret_cast<const i32x4*>(codes + (size_t)(first + st) * kMxBlockBytes);
-        s |= (int)scales[first + st] << (8 * st);
-      } else {
-        s |= 127 << (8 * st);
-      }
-    }
-  };
-  for (int run = wv; run * 16 < p.blocks; run += kDirectWaves) {
-    const int first = run * 16 + 4 * g;
-    i32x4 w[HALVES][4], a[MB][4];
-    int sw[HALVES], sa[MB];
-#pragma unroll
-    for (int h = 0; h < HALVES; ++h) load(wc[h], ws[h], first, w[h], sw[h]);
+  for (int run = wv; run * 16 < p.blocks; run += W) {
+    i32x4 a[MB][4];
+    int sa[MB];
 #pragma unroll
     for (int b = 0; b < MB; ++b) load(ac[b], as[b], first, a[b], sa[b]);
 #pragma unroll
@@ -208,6 +226,11 @@ __global__ __launch_bounds__(kDirectWaves * 64) void direct_kernel(MxMatmulParam
         acc[h][b] = mfma_fp4<2>(w[h][2], a[b][2], acc[h][b], sw[h], sa[b]);
         acc[h][b] = mfma_fp4<3>(w[h][3], a[b][3], acc[h][b], sw[h], sa[b]);
       }
+    first += W * 16;
+    if ((run + W) * 16 < p.blocks) {
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h) load(wc[h], ws[h], first, w[h], sw[h]);
+    }
   }
 #pragma unroll
   for (int h = 0; h < HALVES; ++h)
@@ -215,7 +238,7 @@ __global__ __launch_bounds__(kDirectWaves * 64) void direct_kernel(MxMatmulParam
     for (int b = 0; b < MB; ++b) red[wv][h * MB + b][lane] = acc[h][b];
   __syncthreads();
   // Lane j + 16 g of fragment b holds weight rows n0 + 4g .. + 3 of activation row 16 b + j.
-  for (int q = threadIdx.x; q < MB * 64; q += kDirectWaves * 64) {
+  for (int q = threadIdx.x; q < MB * 64; q += W * 64) {
     const int b = q >> 6, ln = q & 63;
     const int r = tile_row(p, start, len, 16 * b + (ln & 15));
     if (r < 0) continue;
@@ -223,7 +246,8 @@ __global__ __launch_bounds__(kDirectWaves * 64) void direct_kernel(MxMatmulParam
 #pragma unroll
     for (int h = 0; h < HALVES; ++h) {
       y[h] = red[0][h * MB + b][ln];
-      for (int u = 1; u < kDirectWaves; ++u) y[h] += red[u][h * MB + b][ln];
+#pragma unroll
+      for (int u = 1; u < W; ++u) y[h] += red[u][h * MB + b][ln];
     }
     float v[4];
 #pragma unroll
@@ -238,83 +262,143 @@ __global__ __launch_bounds__(kDirectWaves * 64) void direct_kernel(MxMatmulParam
   }
 }
 
-template <int MB>
+template <int MB, int HALVES, int W>
 hipError_t launch_direct(const MxMatmulParams& p, hipStream_t stream) {
   int64_t tiles = (p.m + MB * 16 - 1) / (MB * 16);
   // an expert's last tile may be partly filled: at most one more per expert that has pairs
   if (p.offsets) tiles = p.m / (MB * 16) + (p.m < p.E ? p.m : p.E);
   const int64_t grid = tiles * ((p.n + 15) / 16);
   if (grid >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
-  if (p.w1)
-    hipLaunchKernelGGL((direct_kernel<MB, 2>), dim3((unsigned)grid), dim3(kDirectWaves * 64), 0, stream, p);
+  if (p.blocks % 16 == 0)
+    hipLaunchKernelGGL((direct_kernel<MB, HALVES, W, false>), dim3((unsigned)grid), dim3(W * 64), 0, stream, p);
   else
-    hipLaunchKernelGGL((direct_kernel<MB, 1>), dim3((unsigned)grid), dim3(kDirectWaves * 64), 0, stream, p);
+    hipLaunchKernelGGL((direct_kernel<MB, HALVES, W, true>), dim3((unsigned)grid), dim3(W * 64), 0, stream, p);
   return hipGetLastError();
 }
 
-
 // ---- the tiled kernel -----------------------------------------------------------------------
 // A workgroup of WM x WN waves computes BM activation rows by BN weight rows (with two matrices
-// BN / 2 rows of each, so that a wave holds both factors of its outputs).  Stages of 256 inputs
-// (128 bytes a row) go from memory to LDS without passing registers, NST - 1 stages ahead of the
-// one being multiplied; rows and blocks past the operands' ends are given an offset past the
-// buffer's range, for which the load writes zeros.
+// BN / 2 rows of each, so that a wave holds both factors of its outputs).  Stages of KS * 128 inputs
+// go from memory to LDS without passing registers, NST - 1 stages ahead of the one being
+// multiplied; rows and blocks past the operands' ends are given an offset past the buffer's range,
+// for which the load writes zeros.
 //
-// The 16-byte blocks of a row are stored so that the 16 lanes of an LDS read phase touch 16
-// different 16-byte columns: the block 2g + st of a stage (lane group g, instruction st) lies at
-// place (g + 4 st) ^ ((row / 2) % 8).
+// Instruction st of a stage takes block KS g + st of lane group g.  A row's 16-byte blocks are
+// stored so that the 16 lanes of an LDS read phase (rows 0-3, 12-15 of one lane group and rows 4-11
+// of the next, or the other way round) touch 16 different 16-byte columns of the banks: see place_of.
 //
-// Scales take the way through registers, four stages (32 bytes a row) at a time, double-buffered.
+// Scales take the way through registers, 16 blocks (a window: four instructions) at a time,
+// double-buffered.  A lane group's four bytes go side by side, so that a fragment's scales of a
+// window are one linear LDS read of 256 bytes.  (Read as they come, two bytes at a row's distance
+// of 32, they cost the LDS more than the codes: half of its busy cycles at 8192^3.)
 typedef __attribute__((address_space(3))) void lds_void;
 
-constexpr int kStageBlocks = 8;           // 32-value blocks of a row in a stage
-constexpr int kStageBytes = 128;          // their codes
-constexpr int kWindow = 4;                // stages whose scales are loaded together
-constexpr int kWindowBytes = kWindow * kStageBlocks;
+constexpr int kWindowBlocks = 16;         // blocks of a row whose scales are loaded together
 constexpr uint32_t kNoRow = 0x80000000u;  // a byte offset past every buffer resource's range
+
+template <int I> struct Step { static constexpr int value = I; };
 
 __device__ inline __amdgpu_buffer_rsrc_t mx_rsrc(const uint8_t* base) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), (short)0, 0x7fffffff, 0x00020000);
 }
 
-// The 32 scale bytes of one row's window from block `first` on; 127 (a factor of one, for the zero
-// codes) past the row's end.  Rows of scales need no alignment: the loads are dwords of any address,
-// those at the row's end moved back to end with it (blocks >= 4).  No branches: a branch in the loop
-// over stages lets the compiler sink the products of all stages behind the last one.
-__device__ inline void load_window(const uint8_t* row, int first, int blocks, uint32_t (&s)[8]) {
-  typedef uint32_t __attribute__((aligned(1))) u32_any;
+// Place of lane group g's block for instruction st in LDS row `row`, in 16-byte units.
+template <int KS>
+__device__ inline int place_of(int row, int g, int st) {
+  if (KS == 2) return (g + 4 * st) ^ ((row >> 1) & 7);
+  return g ^ ((0x78 >> (2 * ((row >> 2) & 3))) & 3);  // 0 2 3 1
+}
+
+// The block of a stage that lies at `place` of LDS row `row`: place_of's inverse.
+template <int KS>
+__device__ inline int block_at(int row, int place) {
+  if (KS == 2) {
+    const int q = place ^ ((row >> 1) & 7);
+    return 2 * (q & 3) + (q >> 2);
+  }
+  return place ^ ((0x78 >> (2 * ((row >> 2) & 3))) & 3);
+}
+
+// The 16 scale bytes from byte `at` of a matrix's `size` on (size >= 16), of which the first `left`
+// (at most 16, none if negative) belong to the row; the others become 127, a factor of one for the
+// zero codes there.  One load of any alignment, moved back where it would pass the matrix's end; its
+// bytes are moved on afterwards.  (Four loads of a dword each cost the address unit four times as
+// many cache lines.)  No branches: a branch in the loop over stages lets the compiler sink the
+// products of all stages behind the last one.
+struct __attribute__((packed, aligned(1))) Bytes16 { uint32_t w[4]; };
+
+__device__ inline void load_window(const uint8_t* scales, int64_t at, int64_t size, uint32_t (&s)[4]) {
+  const Bytes16 v = *reinterpret_cast<const Bytes16*>(scales + min(at, size - 16));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int at = first + 4 * i;
-    s[i] = *reinterpret_cast<const u32_any*>(row + min(at, blocks - 4));
+  for (int i = 0; i < 4; ++i) s[i] = v.w[i];
+}
+
+__device__ inline void trim_window(int64_t at, int64_t size, int left, uint32_t (&s)[4]) {
+  const int back = (int)min(max(at - (size - 16), (int64_t)0), (int64_t)15);
+  typedef unsigned __int128 u128;
+  const u128 v = (((u128)s[3] << 96) | ((u128)s[2] << 64) | ((u128)s[1] << 32) | s[0]) >> (8 * back);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = (uint32_t)(v >> (32 * i));
+    const int in = min(max(left - 4 * i, 0), 4);  // bytes inside the row
+    const uint32_t mask = (uint32_t)(((uint64_t)1 << (8 * in)) - 1);
+    s[i] = (w & mask) | (0x7f7f7f7fu & ~mask);
   }
 }
 
-__device__ inline void trim_window(int first, int blocks, uint32_t (&s)[8]) {
+// Byte order of a window in LDS: dword g holds lane group g's bytes in the order of instructions.
+template <int KS>
+__device__ inline i32x4 window_order(const uint32_t (&s)[4]) {
+  i32x4 d;
+  if (KS == 2) {  // instruction 2 t + st takes byte 8 t + 2 g + st
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int left = min(max(blocks - (first + 4 * i), 0), 4);  // bytes inside the row
-    const uint32_t v = (uint32_t)(((uint64_t)s[i]) >> (8 * (4 - left)));
-    const uint32_t mask = (uint32_t)(((uint64_t)1 << (8 * left)) - 1);
-    s[i] = (v & mask) | (0x7f7f7f7fu & ~mask);
+    for (int g = 0; g < 4; ++g)
+      d[g] = (int)(g & 1 ? (s[g / 2] >> 16) | (s[2 + g / 2] & 0xffff0000u) : (s[g / 2] & 0xffffu) | (s[2 + g / 2] << 16));
+  } else {  // instruction t takes byte 4 t + g
+    const uint32_t a = __builtin_amdgcn_perm(s[1], s[0], 0x05010400), b = __builtin_amdgcn_perm(s[3], s[2], 0x05010400);
+    const uint32_t c = __builtin_amdgcn_perm(s[1], s[0], 0x07030602), e = __builtin_amdgcn_perm(s[3], s[2], 0x07030602);
+    d[0] = (int)((a & 0xffffu) | (b << 16));
+    d[1] = (int)((a >> 16) | (b & 0xffff0000u));
+    d[2] = (int)((c & 0xffffu) | (e << 16));
+    d[3] = (int)((c >> 16) | (e & 0xffff0000u));
   }
+  return d;
 }
 
-template <int BM, int BN, int WM, int WN, int NST, int HALVES>
+// Waits until at most FLY vector memory operations are outstanding and LDS operations are done.
+template <int FLY>
+__device__ inline void wait_loads() {
+  static_assert(FLY < 64, "");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((FLY & 15) | (FLY >> 4) << 14 | 7 << 4);
+  asm volatile("" ::: "memory");
+}
+
+__device__ inline void wave_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <int BM, int BN, int WM, int WN, int NST, int KS, int HALVES>
 __global__ __launch_bounds__(WM * WN * 64) void tiled_kernel(MxMatmulParams p, int tiles, int row_blocks) {
   constexpr int kThreads = WM * WN * 64;
   constexpr int kRows = BM + BN;                     // rows of a stage: activations, then weights
-  constexpr int kLoads = kRows * 8 / kThreads;       // 16-byte loads of a thread and stage
+  constexpr int kStageBlocks = 4 * KS;               // 32-value blocks of a row in a stage
+  constexpr int kStageBytes = kStageBlocks * kMxBlockBytes;
+  constexpr int kLoads = kRows * kStageBlocks / kThreads;  // 16-byte loads of a thread and stage
   constexpr int kScaleRows = (kRows + kThreads - 1) / kThreads;
+  constexpr int kWindow = 4 / KS;                    // stages of a window
   constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
   constexpr int FH = FN / HALVES;                    // fragments of one matrix
   constexpr bool kPair = FH % 2 == 0;                // two fragments side by side: 8 outputs in a lane
-  static_assert(kRows * 8 % kThreads == 0 && (NST == 2 || NST == 4), "");
+  static_assert(kRows * kStageBlocks % kThreads == 0 && BM * kStageBlocks % kThreads == 0, "a load is of one operand");
+  static_assert((NST == 2 || NST == 4) && FH >= 1, "");
   __shared__ __attribute__((aligned(1024))) uint8_t c0[kRows * kStageBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t c1[kRows * kStageBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t c2[NST > 2 ? kRows * kStageBytes : 16];
   __shared__ __attribute__((aligned(1024))) uint8_t c3[NST > 2 ? kRows * kStageBytes : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t sc[2][kRows * kWindowBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t sc[2][kRows * kWindowBlocks];
 
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wv / WN, wn = wv % WN;
@@ -353,13 +437,18 @@ __global__ __launch_bounds__(WM * WN * 64) void tiled_kernel(MxMatmulParams p, i
   const __amdgpu_buffer_rsrc_t rw0 = mx_rsrc(p.w0 + w_base);
   const __amdgpu_buffer_rsrc_t rw1 = mx_rsrc(HALVES == 2 ? p.w1 + w_base : p.w0 + w_base);
 
+  // Load i of a thread: LDS row and block of the stage.
+  auto load_at = [&](int i, int& r, int& block) {
+    const int slot = i * kThreads + tid;
+    r = slot / kStageBlocks;
+    block = block_at<KS>(r, slot % kStageBlocks);
+  };
   uint32_t off[kLoads];
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
-    const int slot = i * kThreads + tid, r = slot >> 3;
-    const int place = (slot & 7) ^ ((r >> 1) & 7);
-    const int block = 2 * (place & 3) + (place >> 2);
-    if (i * kThreads < BM * 8) {
+    int r, block;
+    load_at(i, r, block);
+    if (i * kThreads < BM * kStageBlocks) {
       const int row = act_row(r);
       off[i] = row < 0 ? kNoRow : (uint32_t)((size_t)(row - a_base) * row_codes) + block * kMxBlockBytes;
     } else {
@@ -368,54 +457,57 @@ __global__ __launch_bounds__(WM * WN * 64) void tiled_kernel(MxMatmulParams p, i
       off[i] = row < p.n ? (uint32_t)((size_t)(row - n0) * row_codes) + block * kMxBlockBytes : kNoRow;
     }
   }
-  static_assert(BM * 8 % kThreads == 0, "a load index is of one operand");
   const int stages = (blocks + kStageBlocks - 1) / kStageBlocks;
   auto issue = [&](uint8_t* dst, int s) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       // blocks past the row's end, and stages past the last
-      const int slot = i * kThreads + tid, place = (slot & 7) ^ ((slot >> 4) & 7);
-      const uint32_t o = s * kStageBlocks + 2 * (place & 3) + (place >> 2) < blocks ? off[i] : kNoRow;
+      int r, block;
+      load_at(i, r, block);
+      const uint32_t o = s * kStageBlocks + block < blocks ? off[i] : kNoRow;
       const int so = min(s, stages) * kStageBytes;
       lds_void* at = (lds_void*)(dst + (i * kThreads + wv * 64) * 16);
-      if (i * kThreads < BM * 8) {
+      if (i * kThreads < BM * kStageBlocks) {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, at, 16, o, so, 0, 0);
       } else {
-        int half = 0;  // a wave's load is of 8 rows of one fragment, so of one matrix
-        if (HALVES == 2) weight_row((i * kThreads + wv * 64) / 8 - BM, half);
+        int half = 0;  // a wave's load is of rows of one fragment, so of one matrix
+        if (HALVES == 2) weight_row((i * kThreads + wv * 64) / kStageBlocks - BM, half);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(half ? rw1 : rw0, at, 16, o, so, 0, 0);
       }
     }
   };
 
   // A row that is not there reads another row's scales: they reach only outputs that are not stored.
-  const uint8_t* srow[kScaleRows];
+  const uint8_t* sbase[kScaleRows];
+  int64_t srow[kScaleRows], ssize[kScaleRows];
 #pragma unroll
   for (int i = 0; i < kScaleRows; ++i) {
     const int r = min(i * kThreads + tid, kRows - 1);
     if (r < BM) {
-      srow[i] = p.a_scale + (size_t)max(act_row(r), 0) * blocks;
+      sbase[i] = p.a_scale;
+      srow[i] = (int64_t)max(act_row(r), 0) * blocks;
+      ssize[i] = (int64_t)p.a_rows * blocks;
     } else {
       int half;
       const int row = min(weight_row(r - BM, half), p.n - 1);
-      srow[i] = (half ? p.w1_scale : p.w0_scale) + ((size_t)expert * p.n + row) * blocks;
+      sbase[i] = half ? p.w1_scale : p.w0_scale;
+      srow[i] = ((int64_t)expert * p.n + row) * blocks;
+      ssize[i] = (int64_t)p.E * p.n * blocks;
     }
   }
-  uint32_t sreg[kScaleRows][8];
+  uint32_t sreg[kScaleRows][4];
   auto scales_load = [&](int window) {
 #pragma unroll
-    for (int i = 0; i < kScaleRows; ++i) load_window(srow[i], window * kWindowBytes, blocks, sreg[i]);
+    for (int i = 0; i < kScaleRows; ++i)
+      load_window(sbase[i], srow[i] + min(window * kWindowBlocks, blocks), ssize[i], sreg[i]);
   };
   auto scales_store = [&](int window) {
 #pragma unroll
     for (int i = 0; i < kScaleRows; ++i) {
-      trim_window(window * kWindowBytes, blocks, sreg[i]);
+      const int first = min(window * kWindowBlocks, blocks);
+      trim_window(srow[i] + first, ssize[i], blocks - first, sreg[i]);
       const int r = min(i * kThreads + tid, kRows - 1);  // threads past the rows write the last one's again
-      {
-        i32x4* d = reinterpret_cast<i32x4*>(&sc[window & 1][r * kWindowBytes]);
-        d[0] = i32x4{(int)sreg[i][0], (int)sreg[i][1], (int)sreg[i][2], (int)sreg[i][3]};
-        d[1] = i32x4{(int)sreg[i][4], (int)sreg[i][5], (int)sreg[i][6], (int)sreg[i][7]};
-      }
+      *reinterpret_cast<i32x4*>(&sc[window & 1][r * kWindowBlocks]) = window_order<KS>(sreg[i]);
     }
   };
 
@@ -425,46 +517,52 @@ __global__ __launch_bounds__(WM * WN * 64) void tiled_kernel(MxMatmulParams p, i
 #pragma unroll
     for (int b = 0; b < FN; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const int key = (j >> 1) & 7;
   const int a_row = wm * (BM / WM) + j, w_row = BM + wn * (BN / WN) + j;
-  auto multiply = [&](const uint8_t* cur, int window, int step) {
-    const uint8_t* ss = &sc[window & 1][step * kStageBlocks + 2 * g];
-    int sa[FM], sw[FN];
+  int sa[FM], sw[FN];  // scales of a window
+  auto read_scales = [&](int window) {
+    const uint8_t* ss = &sc[window & 1][4 * g];
 #pragma unroll
-    for (int a = 0; a < FM; ++a) sa[a] = *reinterpret_cast<const uint16_t*>(ss + (a_row + 16 * a) * kWindowBytes);
+    for (int a = 0; a < FM; ++a) sa[a] = *reinterpret_cast<const int*>(ss + (a_row + 16 * a) * kWindowBlocks);
 #pragma unroll
-    for (int b = 0; b < FN; ++b) sw[b] = *reinterpret_cast<const uint16_t*>(ss + (w_row + 16 * b) * kWindowBytes);
-#pragma unroll
-    for (int st = 0; st < 2; ++st) {
-      __builtin_amdgcn_sched_barrier(0);  // one instruction step's fragments at a time in registers
-      const int col = ((g + 4 * st) ^ key) * 16;
-      i32x4 fa[FM], fw[FN];
-#pragma unroll
-      for (int a = 0; a < FM; ++a) fa[a] = *reinterpret_cast<const i32x4*>(cur + (a_row + 16 * a) * kStageBytes + col);
-#pragma unroll
-      for (int b = 0; b < FN; ++b) fw[b] = *reinterpret_cast<const i32x4*>(cur + (w_row + 16 * b) * kStageBytes + col);
-#pragma unroll
-      for (int a = 0; a < FM; ++a)
-#pragma unroll
-        for (int b = 0; b < FN; ++b)
-          acc[a][b] = st == 0 ? mfma_fp4<0>(fw[b], fa[a], acc[a][b], sw[b], sa[a])
-                              : mfma_fp4<1>(fw[b], fa[a], acc[a][b], sw[b], sa[a]);
-    }
+    for (int b = 0; b < FN; ++b) sw[b] = *reinterpret_cast<const int*>(ss + (w_row + 16 * b) * kWindowBlocks);
   };
-  // One stage: wait for its codes (the stages after it stay in flight) and for every wave to have
-  // read the stage whose place the next load takes, start that load, multiply.
-  auto stage = [&](const uint8_t* cur, uint8_t* next, int s0, int step) {  // stage s0 + step, s0 % 4 == 0
-    const int s = s0 + step;
-    constexpr int kFly = (NST - 2) * kLoads;
-    static_assert(kFly < 64, "");
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt((kFly & 15) | (kFly >> 4) << 14 | 7 << 4);  // vmcnt(kFly) lgkmcnt(0)
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+  i32x4 fa[FM], fw[FN];
+  auto read_fragments = [&](const uint8_t* cur, int st) {
+    const int col = place_of<KS>(j, g, st) * 16;  // rows 16 apart have the same order of places
+#pragma unroll
+    for (int b = 0; b < FN; ++b) fw[b] = *reinterpret_cast<const i32x4*>(cur + (w_row + 16 * b) * kStageBytes + col);
+#pragma unroll
+    for (int a = 0; a < FM; ++a) fa[a] = *reinterpret_cast<const i32x4*>(cur + (a_row + 16 * a) * kStageBytes + col);
+  };
+  auto multiply = [&](auto byte) {  // the scales' byte of this instruction step
+#pragma unroll
+    for (int a = 0; a < FM; ++a)
+#pragma unroll
+      for (int b = 0; b < FN; ++b)
+        acc[a][b] = mfma_fp4<decltype(byte)::value>(fw[b], fa[a], acc[a][b], sw[b], sa[a]);
+  };
+
+  // One stage of a window, at its place `step` there.  Before a stage is read, its codes have to have
+  // arrived (the stages after it stay in flight) and every wave has to have read the stage whose
+  // place the next load takes.
+  auto stage = [&](const uint8_t* cur, uint8_t* next, int s, auto step_of_window) {
+    constexpr int step = decltype(step_of_window)::value;
+    const int window = s / kWindow;
+    wait_loads<(NST - 2) * kLoads>();
+    wave_barrier();
     issue(next, s + NST - 1);
-    if (step == 0) scales_load(s0 / kWindow + 1);
-    multiply(cur, s0 / kWindow, step);
-    if (step == kWindow - 1) scales_store(s0 / kWindow + 1);
+    if (step == 0) {
+      scales_load(window + 1);
+      read_scales(window);
+    }
+    read_fragments(cur, 0);
+    multiply(Step<KS * step>());
+    if (KS == 2) {
+      __builtin_amdgcn_sched_barrier(0);  // one instruction step's fragments at a time in registers
+      read_fragments(cur, 1);
+      multiply(Step<KS * step + KS - 1>());
+    }
+    if (step == kWindow - 1) scales_store(window + 1);
   };
 
   scales_load(0);
@@ -474,18 +572,18 @@ __global__ __launch_bounds__(WM * WN * 64) void tiled_kernel(MxMatmulParams p, i
     issue(c2, 2);
   }
   scales_store(0);
-  // Whole windows: up to three stages past the last one multiply zeros.
-  for (int s = 0; s < stages; s += kWindow) {
-    if (NST == 2) {
-      stage(c0, c1, s, 0);
-      stage(c1, c0, s, 1);
-      stage(c0, c1, s, 2);
-      stage(c1, c0, s, 3);
-    } else {
-      stage(c0, c3, s, 0);
-      stage(c1, c0, s, 1);
-      stage(c2, c1, s, 2);
-      stage(c3, c2, s, 3);
+  // Whole turns: the stages past the last one multiply zeros.
+  if (NST == 2 && KS == 2) {
+    for (int s = 0; s < stages; s += 2) {
+      stage(c0, c1, s, Step<0>());
+      stage(c1, c0, s + 1, Step<1 % kWindow>());
+    }
+  } else {
+    for (int s = 0; s < stages; s += 4) {
+      stage(c0, NST == 2 ? c1 : c3, s, Step<0>());
+      stage(c1, c0, s + 1, Step<1 % kWindow>());
+      stage(NST == 2 ? c0 : c2, c1, s + 2, Step<2 % kWindow>());
+      stage(NST == 2 ? c1 : c3, NST == 2 ? c0 : c2, s + 3, Step<3 % kWindow>());
     }
   }
   __builtin_amdgcn_s_waitcnt(0);  // no load to LDS outlives the workgroup
@@ -517,14 +615,14 @@ __global__ __launch_bounds__(WM * WN * 64) void tiled_kernel(MxMatmulParams p, i
     write([&](int r, int c, const float (&v)[kSpan]) { store_f32<kSpan>(p, r, c, v); });
 }
 
-template <int BM, int BN, int WM, int WN, int NST, int HALVES>
+template <int BM, int BN, int WM, int WN, int NST, int KS, int HALVES>
 hipError_t launch_tiled(const MxMatmulParams& p, hipStream_t stream) {
   int64_t tiles = (p.m + BM - 1) / BM;
   if (p.offsets) tiles = p.m / BM + (p.m < p.E ? p.m : p.E);
   const int64_t row_blocks = (p.n + BN / HALVES - 1) / (BN / HALVES);
   const int64_t grid = (tiles + kXcds - 1) / kXcds * kXcds * row_blocks;
   if (grid >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((tiled_kernel<BM, BN, WM, WN, NST, HALVES>), dim3((unsigned)grid), dim3(WM * WN * 64), 0, stream,
+  hipLaunchKernelGGL((tiled_kernel<BM, BN, WM, WN, NST, KS, HALVES>), dim3((unsigned)grid), dim3(WM * WN * 64), 0, stream,
                      p, (int)tiles, (int)row_blocks);
   return hipGetLastError();
 }
@@ -533,11 +631,20 @@ template <int HALVES>
 hipError_t launch_halves(const MxMatmulParams& p, hipStream_t stream) {
   // rows of a full tile: pairs an expert gets on average, or all rows
   const int fill = p.offsets ? (p.m + p.E - 1) / p.E : p.m;
-  if (p.m <= 16) return launch_direct<1>(p, stream);
-  // the tiled kernel reads scales by dwords and addresses a tile's rows by 31-bit offsets
-  if (p.blocks < 4 || p.blocks >= 1 << 18) return launch_direct<4>(p, stream);
-  if (fill <= 64) return launch_tiled<64, 128, 1, 4, 4, HALVES>(p, stream);
-  return launch_tiled<256, 256, 2, 4, 2, HALVES>(p, stream);
+  if (p.m <= 16) return p.blocks >= 128 ? launch_direct<1, HALVES, 8>(p, stream) : launch_direct<1, HALVES, 4>(p, stream);
+  // the tiled kernel reads 16 scales at a time and addresses a tile's rows by 31-bit offsets
+  if ((int64_t)p.a_rows * p.blocks < 16 || (int64_t)p.E * p.n * p.blocks < 16 || p.blocks >= 1 << 18)
+    return launch_direct<4, HALVES, 4>(p, stream);
+  if (!p.offsets) {
+    auto groups = [&](int64_t bm, int64_t bn) { return (p.m + bm - 1) / bm * ((p.n + bn / HALVES - 1) / (bn / HALVES)); };
+    if (p.m <= 32) return launch_direct<2, HALVES, 4>(p, stream);
+    if (groups(256, 256) >= 512) return launch_tiled<256, 256, 2, 4, 4, 1, HALVES>(p, stream);
+    if (groups(128, 128) >= 256) return launch_tiled<128, 128, 2, 2, 2, 2, HALVES>(p, stream);
+    return launch_tiled<32, 128, 1, 4, 2, 2, HALVES>(p, stream);
+  }
+  if (fill <= 32) return launch_tiled<32, 128, 1, 4, 2, 2, HALVES>(p, stream);
+  if (fill <= 128) return launch_tiled<128, 128, 2, 2, 4, 1, HALVES>(p, stream);
+  return launch_tiled<256, 256, 2, 4, 4, 1, HALVES>(p, stream);
 }
 
 }  // namespace
