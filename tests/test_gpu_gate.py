@@ -90,6 +90,17 @@ CASES = [
     (513, 65, 4, dict(num_groups=5, top_groups=2)),
     (40, 320, 16, dict(score="sigmoid", num_groups=2, top_groups=1)),
     (2500, 33, 3, dict(score="sigmoid")),
+    # each side of the kernels' own borders: tokens of one workgroup, of small workgroups, of one pass
+    (16, 256, 4, dict(score="sigmoid")),
+    (17, 256, 9, dict(score="sigmoid", num_groups=4, top_groups=2)),
+    (16, 300, 33 - 1, dict()),
+    (1024, 40, 8, dict(num_groups=2, top_groups=1)),
+    (1025, 40, 9, dict(score="sigmoid")),
+    (4097, 24, 4, dict(num_groups=3, top_groups=2, group_top=2)),
+    (9000, 12, 1, dict(score="sigmoid")),
+    (600, 260, 3, dict(score="sigmoid", num_groups=2, top_groups=1)),
+    (33000, 8, 2, dict()),
+    (8300, 272, 2, dict(score="sigmoid")),
 ]
 
 

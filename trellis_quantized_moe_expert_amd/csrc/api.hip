@@ -881,7 +881,7 @@ qtip_status forward_impl(qtip_moe_plan_t plan, const qtip_moe_weights* w, const 
     // routed and binned inside the gate/up launch below (the "route" stage is empty)
     if ((e = prof_mark(plan, 1, st)) != hipSuccess) return hip_fail(e, "profile event");
   } else if (gate) {
-    e = launch_gate(gate_params(plan, gate, lg, n_tokens, topk_idx, topk_w), st);
+    e = launch_gate(gate_params(plan, gate, lg, n_tokens, topk_idx, topk_w), nullptr, st);
     if (e != hipSuccess) return hip_fail(e, "gate launch");
     if ((e = prof_mark(plan, 1, st)) != hipSuccess) return hip_fail(e, "profile event");
     e = launch_bin(topk_idx, P, d.num_experts, plan->tile_m, counts, offsets, sorted_pair, tile_map, n_tiles,
@@ -1104,7 +1104,7 @@ MxMatmulParams mx_pass_params(const qtip_moe_plan_s* plan, int32_t pass, const q
 }
 
 struct MxWsLayout {
-  size_t topk_idx, topk_w, counts, offsets, sorted_pair, tile_map, n_tiles, x_codes, x_scales, h_codes, h_scales, y,
+  size_t topk_idx, topk_w, counts, offsets, sorted_pair, hist, x_codes, x_scales, h_codes, h_scales, y,
       total;
 };
 
@@ -1118,8 +1118,7 @@ MxWsLayout mx_ws_layout(const qtip_moe_desc& d) {
   L.counts = o;       o = align256(o + (size_t)d.num_experts * 4);
   L.offsets = o;      o = align256(o + ((size_t)d.num_experts + 1) * 4);
   L.sorted_pair = o;  o = align256(o + P * 4);
-  L.tile_map = o;     o = align256(o + P * 12);
-  L.n_tiles = o;      o = align256(o + 4);
+  L.hist = o;         o = align256(o + (size_t)kGateMaxBlocks * d.num_experts * 4);
   L.x_codes = o;      o = align256(o + n * d.hidden / 2);
   L.x_scales = o;     o = align256(o + n * d.hidden / kMxBlock);
   L.h_codes = o;      o = align256(o + P * d.inter / 2);
@@ -1371,7 +1370,7 @@ qtip_status qtip_moe_log_engaged(qtip_moe_plan_t plan, int32_t n_tokens, int32_t
 
 size_t qtip_moe_gate_workspace_bytes(qtip_moe_plan_t plan) {
   if (!plan) return 0;
-  return align256((size_t)plan->d.max_tokens * plan->d.top_k * 12) + 256;
+  return align256((size_t)kGateMaxBlocks * plan->d.num_experts * 4);
 }
 
 qtip_status qtip_moe_gate_route(qtip_moe_plan_t plan, const qtip_moe_gate* gate, const float* logits,
@@ -1392,16 +1391,16 @@ qtip_status qtip_moe_gate_route(qtip_moe_plan_t plan, const qtip_moe_gate* gate,
   int dev = 0;
   if ((s = ensure_device(plan, st, &dev)) != QTIP_OK) return s;
   const qtip_moe_desc& d = plan->d;
-  if (!tile_map) {
-    tile_map = reinterpret_cast<int32_t*>(workspace);
-    n_tiles = tile_map + (size_t)d.max_tokens * d.top_k * 3;
-  }
-  hipError_t e = launch_gate(gate_params(plan, gate, logits, n_tokens, topk_idx, topk_w), st);
+  GateBins bins{};
+  bins.counts = counts;
+  bins.offsets = offsets;
+  bins.sorted_pair = sorted_pair;
+  bins.tile_map = tile_map;
+  bins.n_tiles = n_tiles;
+  bins.tile_m = plan->tile_m;
+  bins.hist = reinterpret_cast<int32_t*>(workspace);
+  const hipError_t e = launch_gate(gate_params(plan, gate, logits, n_tokens, topk_idx, topk_w), &bins, st);
   if (e != hipSuccess) return hip_fail(e, "gate launch");
-  plan->stats.route_launches++;
-  e = launch_bin(topk_idx, n_tokens * d.top_k, d.num_experts, plan->tile_m, counts, offsets, sorted_pair, tile_map,
-                 n_tiles, nullptr, nullptr, nullptr, st);
-  if (e != hipSuccess) return hip_fail(e, "bin launch");
   plan->stats.route_launches++;
   return QTIP_OK;
 }
@@ -1535,8 +1534,6 @@ qtip_status qtip_mx_moe_forward(qtip_moe_plan_t plan, const qtip_mx_weights* w, 
   int32_t* counts = reinterpret_cast<int32_t*>(ws + L.counts);
   int32_t* offsets = reinterpret_cast<int32_t*>(ws + L.offsets);
   int32_t* sorted_pair = reinterpret_cast<int32_t*>(ws + L.sorted_pair);
-  int32_t* tile_map = reinterpret_cast<int32_t*>(ws + L.tile_map);
-  int32_t* n_tiles = reinterpret_cast<int32_t*>(ws + L.n_tiles);
   uint8_t* x_codes = reinterpret_cast<uint8_t*>(ws + L.x_codes);
   uint8_t* x_scales = reinterpret_cast<uint8_t*>(ws + L.x_scales);
   uint8_t* h_codes = reinterpret_cast<uint8_t*>(ws + L.h_codes);
@@ -1545,20 +1542,27 @@ qtip_status qtip_mx_moe_forward(qtip_moe_plan_t plan, const qtip_mx_weights* w, 
   const int32_t P = n_tokens * d.top_k;
 
   hipError_t e;
-  if (!gate && n_tokens <= kFusedRouteMaxTokens) {
-    e = launch_route_bin(logits, 1, n_tokens, d.num_experts, d.top_k, topk_idx, topk_w, plan->tile_m, counts, offsets,
-                         sorted_pair, tile_map, n_tiles, nullptr, nullptr, nullptr, st);
-    if (e != hipSuccess) return hip_fail(e, "route/bin launch");
-    plan->stats.route_launches++;
+  GateBins bins{};
+  bins.counts = counts;
+  bins.offsets = offsets;
+  bins.sorted_pair = sorted_pair;
+  bins.hist = reinterpret_cast<int32_t*>(ws + L.hist);
+  if (gate) {
+    e = launch_gate(gate_params(plan, gate, logits, n_tokens, topk_idx, topk_w), &bins, st);
+    if (e != hipSuccess) return hip_fail(e, "gate launch");
   } else {
-    e = gate ? launch_gate(gate_params(plan, gate, logits, n_tokens, topk_idx, topk_w), st)
-             : launch_route_topk(logits, 1, n_tokens, d.num_experts, d.top_k, topk_idx, topk_w, st);
-    if (e != hipSuccess) return hip_fail(e, "routing launch");
-    e = launch_bin(topk_idx, P, d.num_experts, plan->tile_m, counts, offsets, sorted_pair, tile_map, n_tiles, nullptr,
-                   nullptr, nullptr, st);
+    e = launch_route_topk(logits, 1, n_tokens, d.num_experts, d.top_k, topk_idx, topk_w, st);
+    if (e != hipSuccess) return hip_fail(e, "route_topk launch");
+    GateParams g{};
+    g.n = n_tokens;
+    g.E = d.num_experts;
+    g.k = d.top_k;
+    g.topk_idx = topk_idx;
+    e = launch_gate_bins(g, bins, st);
     if (e != hipSuccess) return hip_fail(e, "bin launch");
-    plan->stats.route_launches += 2;
+    plan->stats.route_launches++;
   }
+  plan->stats.route_launches++;
   MxQuantParams q{};
   q.src = x_bf16;
   q.row_stride = d.hidden;

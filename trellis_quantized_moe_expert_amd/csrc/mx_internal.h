@@ -23,7 +23,22 @@ struct GateParams {
   float* topk_w;        // [n][k]
 };
 
-hipError_t launch_gate(const GateParams& p, hipStream_t stream);
+constexpr int kGateMaxBlocks = 512;  // blocks of tokens whose counts a binning workgroup adds up
+
+struct GateBins {
+  int32_t* counts;       // [E]
+  int32_t* offsets;      // [E + 1]
+  int32_t* sorted_pair;  // [n k]
+  int32_t* tile_map;     // NULL, or [n k][3]
+  int32_t* n_tiles;
+  int32_t tile_m;
+  int32_t* hist;         // [kGateMaxBlocks][E]: scratch of a call with more tokens than a workgroup takes
+};
+
+// bins NULL: the experts and weights only.
+hipError_t launch_gate(const GateParams& p, const GateBins* bins, hipStream_t stream);
+// The bins of experts that another kernel has chosen (p.n, p.E, p.k, p.topk_idx).
+hipError_t launch_gate_bins(const GateParams& p, const GateBins& bins, hipStream_t stream);
 
 // ---- MXFP4 (mx_quant.hip, mx_matmul.hip) -----------------------------------------------------
 constexpr int kMxBlock = 32;       // values that share one scale
