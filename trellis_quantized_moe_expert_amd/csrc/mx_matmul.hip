@@ -627,24 +627,40 @@ hipError_t launch_tiled(const MxMatmulParams& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Which kernel and tile.  Large tiles read the operands less often, small ones make more workgroups;
+// below about one workgroup a CU the second counts more.  Times in us at m x n x k, or pairs of a
+// 256-expert, top-6 layer of 4096 x 2048 (gate+up), each side of a border:
+//   few rows             m = 1: direct; 48 x 4096 x 4096 direct 8.0, 32 x 128 9.0;
+//                        48 x 8192 x 2048 direct 8.2, 32 x 128 7.2
+//   256 x 256 from 256   2048 x 8192 x 2048 (256 tiles) 25.0, 128 x 128 29.6;
+//     workgroups         2048 x 4096 x 4096 (128 tiles) 34.1, 128 x 128 27.2
+//   128 x 128 from 200   1024 x 4096 x 4096 (256) 16.6, 64 x 128 17.6; 512 x 4096 x 4096 (128) 14.8, 11.8
+//   64 x 128 from 256    512 x 4096 x 4096 (256) 11.8, 32 x 128 13.4; 256 x 4096 x 4096 (128) 10.8, 10.1
+//   32 x 64 below 256    256 x 1024 x 8192: 12.2, 32 x 128 15.0
+//     of 32 x 128
+//   experts              6 pairs direct 13.5, 32 x 128 15.8; 12 pairs 21.2, 20.0; 24 pairs an expert 32 x 128 458,
+//                        128 x 128 485; 48 pairs 588, 533; 96 pairs 128 x 128 565, 256 x 256 659; 192 pairs 1050, 752
 template <int HALVES>
 hipError_t launch_halves(const MxMatmulParams& p, hipStream_t stream) {
-  // rows of a full tile: pairs an expert gets on average, or all rows
-  const int fill = p.offsets ? (p.m + p.E - 1) / p.E : p.m;
-  if (p.m <= 16) return p.blocks >= 128 ? launch_direct<1, HALVES, 8>(p, stream) : launch_direct<1, HALVES, 4>(p, stream);
   // the tiled kernel reads 16 scales at a time and addresses a tile's rows by 31-bit offsets
-  if ((int64_t)p.a_rows * p.blocks < 16 || (int64_t)p.E * p.n * p.blocks < 16 || p.blocks >= 1 << 18)
-    return launch_direct<4, HALVES, 4>(p, stream);
-  if (!p.offsets) {
-    auto groups = [&](int64_t bm, int64_t bn) { return (p.m + bm - 1) / bm * ((p.n + bn / HALVES - 1) / (bn / HALVES)); };
-    if (p.m <= 32) return launch_direct<2, HALVES, 4>(p, stream);
-    if (groups(256, 256) >= 512) return launch_tiled<256, 256, 2, 4, 4, 1, HALVES>(p, stream);
-    if (groups(128, 128) >= 256) return launch_tiled<128, 128, 2, 2, 2, 2, HALVES>(p, stream);
-    return launch_tiled<32, 128, 1, 4, 2, 2, HALVES>(p, stream);
+  const bool tiles = (int64_t)p.a_rows * p.blocks >= 16 && (int64_t)p.E * p.n * p.blocks >= 16 && p.blocks < 1 << 18;
+  const int64_t row_blocks = (p.n + 15) / 16;
+  const bool few = p.offsets ? p.m <= 8 || (p.m <= 16 && p.m * row_blocks <= 1280) : p.m <= 16;
+  if (few && !p.offsets && p.blocks >= 128) return launch_direct<1, HALVES, 8>(p, stream);
+  if (few) return launch_direct<1, HALVES, 4>(p, stream);
+  if (!tiles || (!p.offsets && p.m <= 64 && p.n <= 4096)) return launch_direct<2, HALVES, 4>(p, stream);
+  if (p.offsets) {
+    const int fill = (p.m + p.E - 1) / p.E;  // pairs an expert gets on average
+    if (fill <= 28) return launch_tiled<32, 128, 1, 4, 2, 2, HALVES>(p, stream);
+    if (fill <= 160) return launch_tiled<128, 128, 2, 2, 4, 1, HALVES>(p, stream);
+    return launch_tiled<256, 256, 2, 4, 4, 1, HALVES>(p, stream);
   }
-  if (fill <= 32) return launch_tiled<32, 128, 1, 4, 2, 2, HALVES>(p, stream);
-  if (fill <= 128) return launch_tiled<128, 128, 2, 2, 4, 1, HALVES>(p, stream);
-  return launch_tiled<256, 256, 2, 4, 4, 1, HALVES>(p, stream);
+  auto groups = [&](int64_t bm, int64_t bn) { return (p.m + bm - 1) / bm * ((p.n + bn - 1) / bn); };
+  if (groups(256, 256) >= 256) return launch_tiled<256, 256, 2, 4, 4, 1, HALVES>(p, stream);
+  if (groups(128, 128) >= 200) return launch_tiled<128, 128, 2, 2, 2, 2, HALVES>(p, stream);
+  if (groups(64, 128) >= 256) return launch_tiled<64, 128, 1, 4, 2, 2, HALVES>(p, stream);
+  if (groups(32, 128) >= 256) return launch_tiled<32, 128, 1, 4, 2, 2, HALVES>(p, stream);
+  return launch_tiled<32, 64, 1, 2, 4, 2, HALVES>(p, stream);
 }
 
 }  // namespace
