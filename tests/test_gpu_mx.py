@@ -275,3 +275,26 @@ def test_results_do_not_depend_on_the_run():
     for part in ("gate_up", "down"):
         assert np.array_equal(ex.run(part, "fp32"), ex.run(part, "fp32"))
     ex.close()
+
+
+def test_binding_refuses_tensors_that_do_not_hold_the_call():
+    import torch
+    say("mx binding refusals")
+    dev = dict(device="cuda:0")
+    x, c, s = torch.zeros(4, 64, **dev), torch.zeros(4, 32, dtype=torch.uint8, **dev), torch.zeros(
+        4, 2, dtype=torch.uint8, **dev)
+    call = lambda src=x, kind="fp32", rows=4, cols=64, stride=64, codes=c, scales=s, values=None: q.qtip_mx_quantize(
+        src, SRC[kind], rows, cols, stride, 0, codes, scales, values)
+    call()
+    for bad in (dict(src=x.cpu()), dict(kind="bf16"), dict(rows=5), dict(stride=65), dict(codes=c[:3]),
+                dict(scales=s[:, :1]), dict(codes=c.cpu()), dict(values=x[:, :32]), dict(values=x.half())):
+        with pytest.raises(q.QtipError):
+            call(**bad)
+    y = torch.zeros(4, 4, **dev)
+    mm = lambda a=c, sa=s, m=4, w=c, sw=s, n=4, k=64, out=y: q.qtip_mx_matmul(a, sa, m, w, sw, n, k, out, OUT["fp32"])
+    mm()
+    for bad in (dict(a=c.cpu()), dict(m=5), dict(n=5), dict(k=96), dict(out=y.half()), dict(out=y.t()[:2]),
+                dict(sw=s.t().contiguous().t())):
+        with pytest.raises(q.QtipError):
+            mm(**bad)
+    torch.cuda.synchronize()

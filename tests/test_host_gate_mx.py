@@ -124,10 +124,22 @@ def test_expert_matmul_and_layer_refusals(plan):
     assert layer(n=0) == CONFIG and layer(n=65) == CONFIG
 
 
-def test_tensors_in_host_memory_are_refused():
+def test_tensors_in_host_memory_are_refused(plan):
     torch = pytest.importorskip("torch")
-    if not torch.cuda.is_available():
-        pytest.skip("the binding asks torch for the current device")
-    t = torch.zeros(64, dtype=torch.uint8)
-    with pytest.raises(q.QtipError):
-        q.qtip_mx_matmul(t, t, 1, t, t, 1, 32, t, q.QTIP_OUT_F32)
+    t = torch.zeros(1 << 16, dtype=torch.uint8)
+    f = torch.zeros(64)
+    gate, w = q.make_gate(), q.make_weights(*[256] * 7)
+    mw = q.make_mx_weights(*[256] * 6)
+    for call in (lambda: q.qtip_mx_matmul(t, t, 1, t, t, 1, 32, t, q.QTIP_OUT_F32),
+                 lambda: q.qtip_mx_matmul(256, 256, 1, 256, 256, 1, 32, t, q.QTIP_OUT_F32),
+                 lambda: q.qtip_mx_quantize(f, q.QTIP_MX_SRC_F32, 1, 64, 64, 0, 256, 256),
+                 lambda: q.qtip_mx_quantize(256, q.QTIP_MX_SRC_F32, 1, 64, 64, 0, 256, 256, f),
+                 lambda: q.qtip_mx_expert_matmul(plan, 0, mw, t, 256, 256, 256, 1, 256, 0),
+                 lambda: q.qtip_moe_gate_route(plan, gate, f, 1, 256, 256, 256, 256, 256, None, None, 256, 1 << 20),
+                 lambda: q.qtip_moe_gate_route(plan, q.make_gate(bias=f), 256, 1, 256, 256, 256, 256, 256, None, None,
+                                               256, 1 << 20),
+                 lambda: q.qtip_moe_forward_gated(plan, w, gate, t, 256, 1, 256, 256, 1 << 30),
+                 lambda: q.qtip_mx_moe_forward(plan, mw, None, 256, f, 1, 256, 256, 1 << 30)):
+        with pytest.raises(q.QtipError) as ei:
+            call()
+        assert ei.value.status == ARG and ("GPU memory" in str(ei.value) or "device" in str(ei.value))

@@ -191,22 +191,33 @@ def _ptr(obj):
     return int(obj)
 
 
-try:  # torch's own way to the current stream's handle: 0.4 us against 3.6 through the stream object
-    from torch._C import _cuda_getCurrentRawStream as _raw_stream
-except ImportError:
-    _raw_stream = None
+_torch = None       # torch, once it has been needed; None again where it is not installed
+_get_device = None  # torch's current device and its stream's handle as plain calls: 0.4 us a call
+_get_stream = None  # against 3.6 through torch.cuda.current_stream()
+
+
+def _find_torch() -> bool:
+    """Import torch on first use and look its calls up once."""
+    global _torch, _get_device, _get_stream
+    if _torch is None:
+        try:
+            import torch
+        except ImportError:
+            return False
+        _get_device = torch.cuda.current_device
+        _get_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _torch = torch
+    return True
 
 
 def _stream(stream):
     if stream is None:
-        try:
-            import torch
-            if _raw_stream is not None and torch.cuda.is_initialized():
-                return _raw_stream(torch.cuda.current_device())
-            if torch.cuda.is_available():
-                return torch.cuda.current_stream().cuda_stream
-        except ImportError:
-            pass
+        if _torch is None and not _find_torch():
+            return None
+        if _get_stream is not None and _torch.cuda.is_initialized():
+            return _get_stream(_get_device())
+        if _torch.cuda.is_available():
+            return _torch.cuda.current_stream().cuda_stream
         return None
     if hasattr(stream, "cuda_stream"):
         return stream.cuda_stream
@@ -421,23 +432,23 @@ def make_mx_weights(codes_gate=None, scales_gate=None, codes_up=None, scales_up=
 
 def _on_device(fn: str, *items) -> None:
     """Refuse tensors that are not whole arrays in the current GPU's memory: (name, object, bytes)s."""
-    dev = -1
+    if _torch is None and not _find_torch():
+        return
+    dev = None
     for name, obj, size in items:
-        if obj is None or obj.__class__ is int:
+        if obj is None or obj.__class__ is int or not isinstance(obj, _torch.Tensor):
             continue
-        try:
-            where, whole, nbytes = obj.get_device(), obj.is_contiguous(), obj.nbytes
-        except AttributeError:  # an address holder other than a torch tensor
-            continue
-        if dev < 0:
-            import torch
-            dev = torch.cuda.current_device()
+        where = obj.get_device()
+        if where < 0:
+            raise QtipError(fn, QTIP_ERR_INVALID_ARG, f"{name} is not in GPU memory")
+        if dev is None:
+            dev = _get_device()
         if where != dev:
             raise QtipError(fn, QTIP_ERR_INVALID_ARG, f"{name} is not on the current device (cuda:{dev})")
-        if not whole:
-            raise QtipError(fn, QTIP_ERR_INVALID_ARG, f"{name} must be contiguous")
-        if nbytes < size:
+        if obj.nbytes < size:
             raise QtipError(fn, QTIP_ERR_INVALID_ARG, f"{name} is smaller than {size} bytes")
+        if not obj.is_contiguous():
+            raise QtipError(fn, QTIP_ERR_INVALID_ARG, f"{name} must be contiguous")
 
 
 def qtip_moe_gate_workspace_bytes(plan) -> int:
@@ -468,6 +479,14 @@ def qtip_mx_quantize(src, src_type, rows, cols, row_stride, scale_rule, codes, s
                      stream=None) -> None:
     blocks = (cols + QTIP_MX_BLOCK - 1) // QTIP_MX_BLOCK
     size = 4 if src_type == QTIP_MX_SRC_F32 else 2
+    if (_torch is not None or _find_torch()) and isinstance(src, _torch.Tensor):  # rows of a wider tensor are welcome
+        if src.get_device() < 0 or src.get_device() != _get_device():
+            raise QtipError("qtip_mx_quantize", QTIP_ERR_INVALID_ARG, "src is not on the current device")
+        if src.element_size() != size:
+            raise QtipError("qtip_mx_quantize", QTIP_ERR_INVALID_ARG, f"src has no elements of {size} bytes")
+        if src.numel() == 0 or sum((n - 1) * st for n, st in zip(src.shape, src.stride())) < (
+                (rows - 1) * row_stride + cols - 1):
+            raise QtipError("qtip_mx_quantize", QTIP_ERR_INVALID_ARG, "src is smaller than its rows")
     _on_device("qtip_mx_quantize", ("codes", codes, rows * blocks * 16), ("scales", scales, rows * blocks),
                ("values", values, rows * cols * size))
     _check("qtip_mx_quantize", lib().qtip_mx_quantize(_ptr(src), src_type, rows, cols, row_stride, scale_rule,
