@@ -1041,8 +1041,9 @@ qtip_status forward_impl(qtip_moe_plan_t plan, const qtip_moe_weights* w, const 
   if (pp.tok_split) {
     plan->stats.combined_in_down++;  // the "combine" stage is empty
   } else {
-    e = launch_combine(y, topk_w, n_tokens, d.top_k, d.hidden, out, d.out_dtype == QTIP_OUT_BF16, st,
-                       gate ? topk_idx : nullptr, d.num_experts);
+    const int bf16 = d.out_dtype == QTIP_OUT_BF16;
+    e = gate ? launch_combine_chosen(y, topk_w, topk_idx, d.num_experts, n_tokens, d.top_k, d.hidden, out, bf16, st)
+             : launch_combine(y, topk_w, n_tokens, d.top_k, d.hidden, out, bf16, st);
     if (e != hipSuccess) return hip_fail(e, "combine launch");
     plan->stats.combine_launches++;
   }
@@ -1589,8 +1590,8 @@ qtip_status qtip_mx_moe_forward(qtip_moe_plan_t plan, const qtip_mx_weights* w, 
   e = launch_mx_matmul(mx_pass_params(plan, QTIP_MX_PASS_DOWN, w, h_codes, h_scales, offsets, sorted_pair, n_tokens, y,
                                       QTIP_OUT_F32), st);
   if (e != hipSuccess) return hip_fail(e, "MXFP4 down launch");
-  e = launch_combine(y, topk_w, n_tokens, d.top_k, d.hidden, out, d.out_dtype == QTIP_OUT_BF16, st, topk_idx,
-                     d.num_experts);
+  e = launch_combine_chosen(y, topk_w, topk_idx, d.num_experts, n_tokens, d.top_k, d.hidden, out,
+                            d.out_dtype == QTIP_OUT_BF16, st);
   if (e != hipSuccess) return hip_fail(e, "combine launch");
   plan->stats.combine_launches++;
   return QTIP_OK;

@@ -66,11 +66,9 @@ __global__ __launch_bounds__(256) void pack_act_kernel(const uint16_t* __restric
 }
 
 // out[t] = sum_j w[t,j] * y[t*k+j], j ascending, fp32; one thread per 4 outputs.
-// LEFT_OUT: pairs whose expert id lies outside [0, E) were in no bin; their rows of y are skipped.
-template <bool LEFT_OUT>
 __global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ y, const float* __restrict__ w,
-                                                      const int32_t* __restrict__ topk_idx, int32_t E, int32_t n,
-                                                      int32_t k, int32_t H, void* __restrict__ out, int out_bf16) {
+                                                      int32_t n, int32_t k, int32_t H, void* __restrict__ out,
+                                                      int out_bf16) {
   const int h4 = H >> 2;
   const long idx = (long)blockIdx.x * blockDim.x + threadIdx.x;
   if (idx >= (long)n * h4) return;
@@ -80,21 +78,15 @@ __global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ 
   for (int j0 = 0; j0 < k; j0 += 8) {
     float4 v[8];
     float wt[8];
-    bool in[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      in[i] = j0 + i < k;
-      if (LEFT_OUT && in[i]) in[i] = (uint32_t)topk_idx[(size_t)t * k + j0 + i] < (uint32_t)E;
-    }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (in[i]) {
+      if (j0 + i < k) {
         wt[i] = w[(size_t)t * k + j0 + i];
         v[i] = *reinterpret_cast<const float4*>(y + ((size_t)t * k + j0 + i) * H + c);
       }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (in[i]) {
+      if (j0 + i < k) {
         acc.x = fmaf(wt[i], v[i].x, acc.x);
         acc.y = fmaf(wt[i], v[i].y, acc.y);
         acc.z = fmaf(wt[i], v[i].z, acc.z);
@@ -200,11 +192,10 @@ hipError_t launch_dequant(const DequantParams& q, int rung, int grid, hipStream_
 }
 
 hipError_t launch_combine(const float* y, const float* topk_w, int32_t n, int32_t k, int32_t H, void* out,
-                          int out_bf16, hipStream_t stream, const int32_t* topk_idx, int32_t E) {
+                          int out_bf16, hipStream_t stream) {
   const long total = (long)n * (H / 4);
   const int grid = (int)((total + 255) / 256);
-  hipLaunchKernelGGL(topk_idx ? combine_kernel<true> : combine_kernel<false>, dim3(grid), dim3(256), 0, stream, y,
-                     topk_w, topk_idx, E, n, k, H, out, out_bf16);
+  hipLaunchKernelGGL(combine_kernel, dim3(grid), dim3(256), 0, stream, y, topk_w, n, k, H, out, out_bf16);
   return hipGetLastError();
 }
 

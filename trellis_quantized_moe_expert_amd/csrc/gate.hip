@@ -629,6 +629,49 @@ int block_tokens(int n, int pass) {
   return (int)(pass * passes);
 }
 
+// out[t] = sum_j w[t, j] y[t k + j], j ascending, fp32, over the pairs that have an expert: the rows of
+// the others were not written.  A thread takes four neighbouring outputs; up to eight rows' loads are
+// issued before their multiply-adds.
+__global__ __launch_bounds__(256) void combine_chosen_kernel(const float* __restrict__ y, const float* __restrict__ w,
+                                                             const int32_t* __restrict__ topk_idx, int32_t E,
+                                                             int32_t n, int32_t k, int32_t H, void* __restrict__ out,
+                                                             int out_bf16) {
+  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+  const int h4 = H >> 2;
+  const int64_t item = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (item >= (int64_t)n * h4) return;
+  const int t = (int)(item / h4), c = (int)(item - (int64_t)t * h4) * 4;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j0 = 0; j0 < k; j0 += 8) {
+    float4 v[8];
+    float wt[8];
+    bool in[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      in[i] = j0 + i < k && (uint32_t)topk_idx[(size_t)t * k + min(j0 + i, k - 1)] < (uint32_t)E;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (in[i]) {
+        wt[i] = w[(size_t)t * k + j0 + i];
+        v[i] = *reinterpret_cast<const float4*>(y + ((size_t)t * k + j0 + i) * H + c);
+      }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (in[i]) {
+        acc.x = fmaf(wt[i], v[i].x, acc.x);
+        acc.y = fmaf(wt[i], v[i].y, acc.y);
+        acc.z = fmaf(wt[i], v[i].z, acc.z);
+        acc.w = fmaf(wt[i], v[i].w, acc.w);
+      }
+  }
+  const size_t o = (size_t)t * H + c;
+  if (out_bf16)
+    *reinterpret_cast<bf16x4*>(reinterpret_cast<uint16_t*>(out) + o) =
+        bf16x4{(__bf16)acc.x, (__bf16)acc.y, (__bf16)acc.z, (__bf16)acc.w};
+  else
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + o) = acc;
+}
+
 template <int LANES, int Q, int KL, int W>
 hipError_t launch_waves(const GateParams& p, const GateShape& gs, const GateBins* o, hipStream_t stream) {
   constexpr int kPass = W * (64 / LANES);  // tokens of a workgroup at a time
@@ -693,6 +736,14 @@ hipError_t launch_gate_bins(const GateParams& p, const GateBins& bins, hipStream
   }
   hipLaunchKernelGGL(place_kernel, dim3((unsigned)blocks), dim3(kGateWaves * 64), 0, stream, p, bins, per_block,
                      blocks);
+  return hipGetLastError();
+}
+
+hipError_t launch_combine_chosen(const float* y, const float* topk_w, const int32_t* topk_idx, int32_t E, int32_t n,
+                                 int32_t k, int32_t H, void* out, int out_bf16, hipStream_t stream) {
+  const int64_t items = (int64_t)n * (H / 4);
+  hipLaunchKernelGGL(combine_chosen_kernel, dim3((unsigned)((items + 255) / 256)), dim3(256), 0, stream, y, topk_w,
+                     topk_idx, E, n, k, H, out, out_bf16);
   return hipGetLastError();
 }
 

@@ -40,6 +40,10 @@ hipError_t launch_gate(const GateParams& p, const GateBins* bins, hipStream_t st
 // The bins of experts that another kernel has chosen (p.n, p.E, p.k, p.topk_idx).
 hipError_t launch_gate_bins(const GateParams& p, const GateBins& bins, hipStream_t stream);
 
+// The weighted sum of a token's pairs that have an expert (H a multiple of 4).
+hipError_t launch_combine_chosen(const float* y, const float* topk_w, const int32_t* topk_idx, int32_t E, int32_t n,
+                                 int32_t k, int32_t H, void* out, int out_bf16, hipStream_t stream);
+
 // ---- MXFP4 (mx_quant.hip, mx_matmul.hip) -----------------------------------------------------
 constexpr int kMxBlock = 32;       // values that share one scale
 constexpr int kMxBlockBytes = 16;  // their codes

@@ -207,9 +207,8 @@ hipError_t launch_route_bin(const float* logits, int32_t n_part, int32_t n, int3
 hipError_t launch_pack_act(const uint16_t* x, const int32_t* padded_pair, const int32_t* n_pad, int32_t k,
                            int32_t H, int32_t n_pad_max, uint16_t* xs, hipStream_t stream);
 
-// With topk_idx the pairs whose expert id lies outside [0, E) are skipped (their y was not written).
 hipError_t launch_combine(const float* y, const float* topk_w, int32_t n, int32_t k, int32_t H, void* out,
-                          int out_bf16, hipStream_t stream, const int32_t* topk_idx = nullptr, int32_t E = 0);
+                          int out_bf16, hipStream_t stream);
 
 hipError_t launch_witness(int32_t* out, hipStream_t stream);
 
