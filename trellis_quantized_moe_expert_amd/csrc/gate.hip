@@ -22,6 +22,15 @@
 // pairs of lanes merge their best KL until all lanes hold the token's best KL in order.  Where two
 // neighbours of that order (the best one left among them) are equal in fp32, the wave chooses again
 // on the fp64 values.
+//
+// What bounds it: the issue of fp64 instructions, not memory.  16384 tokens of 256 experts, 8 of 8
+// groups' best 4, sigmoid with bias (16.8 MB of logits, 3.9 us at the copy rate) take 20.6 us in the
+// gate and 9.0 in placing, where each of 256 blocks adds up all blocks' counts out of L2; 27.7 for the
+// call.  A wave of four tokens issues about 700 fp64 instructions, half of them in the 256 sigmoids,
+// half in the sort and the merges, at 6.5 to 7 cycles each.  With the constants and lane masks of a
+// loop over tokens kept in vector registers the kernel spilled and took 25.  Small batches are bound by
+// launches and the latency of a chain of dependent steps: a token of 8 in one workgroup 7.3, 683 tokens
+// 5.6 and 7.5.
 #include "mx_internal.h"
 #include "qtip_internal.h"
 
@@ -80,24 +89,34 @@ __device__ inline double lanes_sum(double v) {
   return v;
 }
 
-// exp(x), x <= 700 (-inf and anything that underflows among them), to about one unit in the last place: x = k ln 2 + r, |r| <= ln 2 / 2, and the
-// Taylor polynomial of exp(r) up to r^13 / 13! (the next term is under 2^-57).
-__device__ inline double exp_f64(double x) {
-  x = fmax(x, -1100.0);  // exp is 0 there
-  const double k = rint(x * 1.4426950408889634);
-  double r = fma(k, -0x1.62e42fefa39efp-1, x);
-  r = fma(k, -0x1.abc9e3b39803fp-56, r);  // ln 2 in two parts
-  double y = 1.0 / 6227020800.0;
-  y = fma(y, r, 1.0 / 479001600.0);
-  y = fma(y, r, 1.0 / 39916800.0);
-  y = fma(y, r, 1.0 / 3628800.0);
-  y = fma(y, r, 1.0 / 362880.0);
-  y = fma(y, r, 1.0 / 40320.0);
-  y = fma(y, r, 1.0 / 5040.0);
-  y = fma(y, r, 1.0 / 720.0);
-  y = fma(y, r, 1.0 / 120.0);
-  y = fma(y, r, 1.0 / 24.0);
-  y = fma(y, r, 1.0 / 6.0);
+// What exp_f64 multiplies by, in scalar registers.  The empty statements keep the compiler from moving
+// the constants out of a loop over tokens, where it kept them in vector registers and spilled those.
+struct ExpTerms {
+  double log2e, ln2_hi, ln2_lo, c[11];  // c[i] = 1 / (13 - i)!
+  __device__ inline ExpTerms() {
+    log2e = 1.4426950408889634;
+    ln2_hi = -0x1.62e42fefa39efp-1;
+    ln2_lo = -0x1.abc9e3b39803fp-56;
+    double factorial = 6227020800.0;  // 13!
+#pragma unroll
+    for (int i = 0; i < 11; ++i) {
+      c[i] = 1.0 / factorial;
+      factorial /= 13 - i;
+      asm volatile("" : "+s"(c[i]));
+    }
+    asm volatile("" : "+s"(log2e), "+s"(ln2_hi), "+s"(ln2_lo));
+  }
+};
+
+// exp(x), -1100 <= x <= 700, to about one unit in the last place: x = k ln 2 + r, |r| <= ln 2 / 2, ln 2 in two parts, and the Taylor polynomial of exp(r) up to
+// r^13 / 13! (the next term is under 2^-57).
+__device__ inline double exp_f64(double x, const ExpTerms& m) {
+  const double k = rint(x * m.log2e);
+  double r = fma(k, m.ln2_hi, x);
+  r = fma(k, m.ln2_lo, r);
+  double y = m.c[0];
+#pragma unroll
+  for (int i = 1; i < 11; ++i) y = fma(y, r, m.c[i]);
   y = fma(y, r, 0.5);
   y = fma(y, r, 1.0);
   y = fma(y, r, 1.0);
@@ -111,15 +130,16 @@ __device__ inline double recip_f64(double d) {
   return fma(fma(-d, y, 1.0), y, y);
 }
 
-// The sigmoid of a logit; 0 below -700, where exp(-l) nears the end of fp64's range.
-__device__ inline double sigmoid_f64(float l) {
-  const double s = recip_f64(1.0 + exp_f64(-fmax((double)l, -700.0)));
+// The sigmoid of a logit; 0 below -700, where exp(-l) nears the end of fp64's range, 1 from 700 on.
+__device__ inline double sigmoid_f64(float l, const ExpTerms& m) {
+  const double s = recip_f64(1.0 + exp_f64((double)fminf(fmaxf(-l, -700.0f), 700.0f), m));
   return l < -700.0f ? 0.0 : s;
 }
 
-// A logit's part of a softmax.  l == top also where both are infinite: such logits share the weight.
-__device__ inline double softmax_part(float l, float top) {
-  return l == top ? 1.0 : exp_f64((double)l - (double)top);
+// A logit's part of a softmax, 0 below exp(-1100).  l == top also where both are infinite: such logits
+// share the weight.
+__device__ inline double softmax_part(float l, float top, const ExpTerms& m) {
+  return l == top ? 1.0 : exp_f64(fmax((double)l - (double)top, -1100.0), m);
 }
 
 // How a gate's groups lie on the lanes (host arithmetic).
@@ -296,8 +316,8 @@ __device__ inline void load_four(__amdgpu_buffer_rsrc_t r, int at, float (&v)[Q]
 // them); e0: its first expert.  Its token's logits are at byte `at` of `logits`.  top, inv: a softmax's largest logit and 1 / sum.
 template <int LANES, int Q>
 __device__ __attribute__((always_inline)) inline void token_values(const GateParams& p, const GateShape& gs,
-                                                                   __amdgpu_buffer_rsrc_t logits, int at, int& e0,
-                                                                   float& top, double& inv, double (&c)[Q]) {
+                                                                   __amdgpu_buffer_rsrc_t logits, int at, const ExpTerms& m,
+                                                                   int& e0, float& top, double& inv, double (&c)[Q]) {
   const __amdgpu_buffer_rsrc_t biases = float_rsrc(p.bias, p.bias ? p.E : 0);
   const int l = threadIdx.x & (LANES - 1);
   const int size = p.E / p.groups;
@@ -319,13 +339,13 @@ __device__ __attribute__((always_inline)) inline void token_values(const GatePar
   }
   if (p.sigmoid) {
 #pragma unroll
-    for (int q = 0; q < Q; ++q) c[q] = sigmoid_f64(lg[q]);
+    for (int q = 0; q < Q; ++q) c[q] = sigmoid_f64(lg[q], m);
   } else {
     top = lanes_max<LANES>(top);
     double sum = 0.0;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      const double part = softmax_part(lg[q], top);
+      const double part = softmax_part(lg[q], top, m);
       c[q] = lg[q] > -INFINITY ? part : 0.0;
       sum += c[q];
     }
@@ -360,7 +380,7 @@ __device__ __attribute__((noinline)) Ids<TURNS> choose_again(GateParams p, GateS
   Ids<TURNS> ids;
 #pragma unroll
   for (int i = 0; i < TURNS; ++i) ids.id[i] = -1;
-  token_values<LANES, Q>(p, gs, token_rows<LANES>(p, __builtin_amdgcn_readfirstlane(first)), at, e0, top, inv, c);
+  token_values<LANES, Q>(p, gs, token_rows<LANES>(p, __builtin_amdgcn_readfirstlane(first)), at, ExpTerms(), e0, top, inv, c);
   choose_exact<LANES, Q, TURNS>(p.k, c, e0, ids.id);
   return ids;
 }
@@ -376,6 +396,7 @@ __device__ __attribute__((always_inline)) inline void gate_tokens(const GatePara
   const bool there = t < p.n;
   const int at = sub * p.E * 4;
   const __amdgpu_buffer_rsrc_t logits = token_rows<LANES>(p, first);
+  const ExpTerms terms;
   int id[kTurns];
   float top;
   double inv;
@@ -383,7 +404,7 @@ __device__ __attribute__((always_inline)) inline void gate_tokens(const GatePara
   {
     double c[Q];
     int e0;
-    token_values<LANES, Q>(p, gs, logits, at, e0, top, inv, c);
+    token_values<LANES, Q>(p, gs, logits, at, terms, e0, top, inv, c);
 #pragma unroll
     for (int q = 0; q < Q; ++q) c[q] = c[q] > -INFINITY ? make_key((float)c[q], e0 + q) : 0.0;
 #pragma unroll
@@ -401,7 +422,7 @@ __device__ __attribute__((always_inline)) inline void gate_tokens(const GatePara
 #pragma unroll
   for (int i = 0; i < kTurns; ++i) {
     const float x = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(logits, at + 4 * max(id[i], 0), 0, 0));
-    const double part = p.sigmoid ? sigmoid_f64(x) : softmax_part(x, top) * inv;
+    const double part = p.sigmoid ? sigmoid_f64(x, terms) : softmax_part(x, top, terms) * inv;
     s[i] = id[i] >= 0 ? part : 0.0;
     z += s[i];
   }
@@ -465,7 +486,10 @@ __device__ inline void peers_of(int e, int bits, int& rank, int& group) {
 }
 
 // Places pairs [p0, p0 + count) (ids from `ids`, indexed by pair) of block b of `blocks`; hist NULL:
-// there is one block, and its counts are counted here.  Run by 1024 threads.
+// there is one block, and its counts are counted here.  Run by 1024 threads.  BATCH: times 64 pairs of a
+// wave whose ids are asked for before the first is used (683 tokens of 6 pairs by one workgroup: 7.6 us
+// with 8, 8.6 with 1; a token of 8, which has one load a wave anyway: 7.3 with 1, 7.7 with 8).
+template <int BATCH>
 __device__ __attribute__((always_inline)) inline void bin_block(const GateBins& o, const int32_t* ids, int E, int p0,
                                                                 int count, const int32_t* hist, int blocks, int b,
                                                                 BinLds& s) {
@@ -476,16 +500,26 @@ __device__ __attribute__((always_inline)) inline void bin_block(const GateBins& 
   for (int e = tid; e < E; e += 1024) s.total[e] = s.before[e] = 0;
   const int chunk = ((count + kGateWaves - 1) / kGateWaves + 63) & ~63;
   const int lo = wv * chunk, hi = min(count, lo + chunk);
-  auto expert = [&](int i) {
-    const int e = i < hi ? ids[p0 + i] : E;
-    return e >= 0 && e < E ? e : E;
+  // the wave's pairs in order, 64 at a time: step(place, expert or E)
+  auto each = [&](auto step) {
+    for (int i0 = lo; i0 < hi; i0 += 64 * BATCH) {
+      int id[BATCH];
+#pragma unroll
+      for (int r = 0; r < BATCH; ++r) {
+        const int i = i0 + 64 * r + lane;
+        id[r] = ids[p0 + min(i, hi - 1)];
+        id[r] = i < hi && id[r] >= 0 && id[r] < E ? id[r] : E;
+      }
+#pragma unroll
+      for (int r = 0; r < BATCH; ++r)
+        if (i0 + 64 * r < hi) step(i0 + 64 * r + lane, id[r]);
+    }
   };
-  for (int i = lo; i < hi; i += 64) {
-    const int e = expert(i + lane);
+  each([&](int, int e) {
     int rank, group;
     peers_of(e, bits, rank, group);
     if (e < E && rank == 0) s.wave_cnt[wv][e] += group;
-  }
+  });
   __syncthreads();
   if (hist) {
     // four experts a thread where rows are whole vectors: the loads of a thread are then a batch or two
@@ -556,16 +590,15 @@ __device__ __attribute__((always_inline)) inline void bin_block(const GateBins& 
     if (tid == E - 1) *o.n_tiles = tincl;
   }
   __syncthreads();
-  for (int i = lo; i < hi; i += 64) {
-    const int e = expert(i + lane);
+  each([&](int i, int e) {
     int rank, group;
     peers_of(e, bits, rank, group);
     if (e < E) {
       const int pos = s.wave_cnt[wv][e] + rank;  // every lane reads before the lowest lane advances it
-      o.sorted_pair[pos] = p0 + i + lane;
+      o.sorted_pair[pos] = p0 + i;
       if (rank == 0) s.wave_cnt[wv][e] = pos + group;
     }
-  }
+  });
 }
 
 enum GateMode { kGateOnly, kGateCount, kGateBin };
@@ -598,7 +631,7 @@ __global__ __launch_bounds__(W * 64) void gate_kernel(GateParams p, GateShape gs
   if (MODE == kGateBin) {
     __shared__ BinLds s;
     __syncthreads();  // the workgroup's stores of topk_idx are visible to all of it
-    bin_block(o, p.topk_idx, p.E, 0, p.n * p.k, nullptr, 1, 0, s);
+    bin_block<1>(o, p.topk_idx, p.E, 0, p.n * p.k, nullptr, 1, 0, s);
   }
 }
 
@@ -606,7 +639,7 @@ __global__ __launch_bounds__(kGateWaves * 64) void place_kernel(GateParams p, Ga
   __shared__ BinLds s;
   const int b = blockIdx.x;
   const int t0 = b * per_block, t1 = min(p.n, t0 + per_block);
-  bin_block(o, p.topk_idx, p.E, t0 * p.k, (t1 - t0) * p.k, blocks > 1 ? o.hist : nullptr, blocks, b, s);
+  bin_block<8>(o, p.topk_idx, p.E, t0 * p.k, (t1 - t0) * p.k, blocks > 1 ? o.hist : nullptr, blocks, b, s);
 }
 
 // The counts of each block of tokens whose experts another kernel has chosen.
