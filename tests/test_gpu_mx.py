@@ -125,6 +125,20 @@ def test_product_matches_float64(m, n, k, kind):
     check_product(packed(rng, m, k), packed(rng, n, k), kind)
 
 
+# every tile of the dense product: rows and columns past the tiles' ends, runs of inputs not full
+TILES = [(20, 8200, 96), (130, 4100, 1120), (280, 2056, 96), (290, 2050, 4160), (260, 4104, 2080), (300, 3300, 160),
+         (1000, 2056, 160), (1001, 2063, 288), (1030, 3200, 96), (1100, 3207, 544), (4000, 4100, 64),
+         (3850, 4351, 352)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("m,n,k", TILES)
+def test_large_product_matches_float64(m, n, k, kind):
+    say(f"product {m}x{n}x{k} {kind}")
+    rng = np.random.default_rng(m * 5 + n + k)
+    check_product(packed(rng, m, k), packed(rng, n, k), kind)
+
+
 def test_product_one_block_at_a_time():
     # one nonzero block per row pair at a time shows any mismatch of codes, scales and lanes exactly
     say("product block by block")

@@ -635,9 +635,11 @@ hipError_t launch_tiled(const MxMatmulParams& p, hipStream_t stream) {
 //   256 x 256 from 256   2048 x 8192 x 2048 (256 tiles) 25.0, 128 x 128 29.6;
 //     workgroups         2048 x 4096 x 4096 (128 tiles) 34.1, 128 x 128 27.2
 //   128 x 128 from 200   1024 x 4096 x 4096 (256) 16.6, 64 x 128 17.6; 512 x 4096 x 4096 (128) 14.8, 11.8
-//   64 x 128 from 256    512 x 4096 x 4096 (256) 11.8, 32 x 128 13.4; 256 x 4096 x 4096 (128) 10.8, 10.1
-//   32 x 64 below 256    256 x 1024 x 8192: 12.2, 32 x 128 15.0
-//     of 32 x 128
+//   64 x 128 from 256    512 x 4096 x 4096 (256) 11.8, 32 x 128 13.4; 256 x 4096 x 4096 (128) 10.7, 10.1
+//   32 x 128: four       one workgroup a CU: nobody hides its waits.  256 x 4096 x 4096 (256) four 8.9,
+//     stages up to 256   two 10.1; 300 x 2048 x 4096 (160) 8.7, 9.7; 256 x 8192 x 2048 (512) 10.7, 8.3
+//   32 x 64 below 128    256 x 2048 x 4096 (128) 32 x 64 7.8, 32 x 128 8.3; 64 x 8192 x 2048 (128) 6.8, 6.3;
+//     of 32 x 128        128 x 2048 x 4096 (64) 7.7, 8.2; 128 x 8192 x 2048 (256) 7.3, 6.7
 //   experts              6 pairs direct 13.5, 32 x 128 15.8; 12 pairs 21.2, 20.0; 24 pairs an expert 32 x 128 458,
 //                        128 x 128 485; 48 pairs 588, 533; 96 pairs 128 x 128 565, 256 x 256 659; 192 pairs 1050, 752
 template <int HALVES>
@@ -659,7 +661,8 @@ hipError_t launch_halves(const MxMatmulParams& p, hipStream_t stream) {
   if (groups(256, 256) >= 256) return launch_tiled<256, 256, 2, 4, 4, 1, HALVES>(p, stream);
   if (groups(128, 128) >= 200) return launch_tiled<128, 128, 2, 2, 2, 2, HALVES>(p, stream);
   if (groups(64, 128) >= 256) return launch_tiled<64, 128, 1, 4, 2, 2, HALVES>(p, stream);
-  if (groups(32, 128) >= 256) return launch_tiled<32, 128, 1, 4, 2, 2, HALVES>(p, stream);
+  if (groups(32, 128) > 256) return launch_tiled<32, 128, 1, 4, 2, 2, HALVES>(p, stream);
+  if (groups(32, 128) >= 128) return launch_tiled<32, 128, 1, 4, 4, 2, HALVES>(p, stream);
   return launch_tiled<32, 64, 1, 2, 4, 2, HALVES>(p, stream);
 }
 
