@@ -4,7 +4,9 @@
  * One MoE layer whose experts are gate/up/down matrices stored as 2-bit
  * bitshift-trellis codes.  Pairs (token, expert) are routed and binned by
  * expert into m-tiles; every woken expert's packed bytes are decoded inside the
- * multiply, so dense weights never exist in memory.
+ * multiply, so dense weights never exist in memory.  The layer can also route through a gate
+ * (scores, a balance bias, groups), and its experts can be MXFP4 matrices (4-bit microscaled
+ * values) on the scaled matrix instructions instead of trellis codes.
  *
  * Sources (the pages this library implements):
  *  - m-tile occupancy page, PR #167 "gate the trellis grouped GEMM on m-tile
@@ -31,7 +33,8 @@
  *    enqueued work that writes every element of its outputs; no call returns
  *    QTIP_OK after a failed launch (launch status is read back with
  *    hipGetLastError after each launch, mapped to QTIP_ERR_HIP, and the HIP
- *    error text is available from qtip_last_error_detail()).
+ *    error text is available from qtip_last_error_detail()).  The entry points that route
+ *    through a gate leave the places of pairs without an expert unwritten; they say so.
  *  - bf16 and fp16 values are passed as their 16-bit patterns.
  *
  * Weight formats (readings of the pages, which give only "packed 2-bit bytes" and name two
@@ -425,9 +428,9 @@ typedef struct qtip_moe_gate {
 
 /* Routes and bins n tokens (the outputs of qtip_moe_route) through a gate.  tile_map and n_tiles may
  * both be NULL.  workspace: qtip_moe_gate_workspace_bytes(plan) bytes, 256-byte aligned, contents
- * need no initialisation; two calls that may overlap need one each.  Errors as qtip_moe_route; a bad
- * gate, one of tile_map and n_tiles NULL without the other, a small or misaligned workspace ->
- * INVALID_ARG.  qtip_moe_gate_workspace_bytes: host only; 0 for a NULL plan. */
+ * need no initialisation; two calls, or replays of two captured graphs, that may overlap need one
+ * each.  Errors as qtip_moe_route; a bad gate, one of tile_map and n_tiles NULL without the other, a
+ * small or misaligned workspace -> INVALID_ARG.  qtip_moe_gate_workspace_bytes: host only; 0 for a NULL plan. */
 size_t qtip_moe_gate_workspace_bytes(qtip_moe_plan_t plan);
 qtip_status qtip_moe_gate_route(qtip_moe_plan_t plan, const qtip_moe_gate* gate /*host struct*/, const float* logits,
                                 int32_t n_tokens, int32_t* topk_idx, float* topk_w, int32_t* counts,
@@ -461,7 +464,7 @@ qtip_status qtip_moe_forward_gated(qtip_moe_plan_t plan, const qtip_moe_weights*
  *   sign is x's.  A block with a NaN or an infinity gets the scale byte 255 and zero codes: it stands
  *   for 32 NaNs.  The last block of a row counts as filled up with zeros.
  *   src [rows] rows of cols elements, row_stride >= cols elements apart, aligned to its type; codes and
- *   values 16-byte aligned.  rows and cols >= 1 (else INVALID_CONFIG), rows x blocks below 2^31.
+ *   values 16-byte aligned.  rows and cols >= 1 (else INVALID_CONFIG), rows x blocks at most 2^30 - 64.
  *   Errors: NULL src, codes or scales, a bad type or rule, row_stride < cols, misalignment, too many
  *   blocks -> INVALID_ARG; else as qtip_moe_route. */
 enum { QTIP_MX_SRC_BF16 = 0, QTIP_MX_SRC_F16 = 1, QTIP_MX_SRC_F32 = 2 };
@@ -475,7 +478,9 @@ qtip_status qtip_mx_quantize(const void* src, int32_t src_type, int32_t rows, in
  * qtip_mx_quantize filled up has k = 32 x its blocks).  A NaN scale makes the outputs of its row NaN.
  * codes 16-byte aligned, scales 4-byte aligned, out 16-byte aligned.  m, n, k >= 1 (else
  * INVALID_CONFIG); m x k and n x k below 2^37, m x n below 2^40.  Errors: NULL, a bad out_dtype, k % 32,
- * misalignment, sizes past the limits -> INVALID_ARG; else as qtip_moe_route. */
+ * misalignment, sizes past the limits -> INVALID_ARG; a launch of 2^32 threads or more (no less than
+ * 2^23 blocks of 16 rows of w for m <= 16, about 2^23 tiles of 256 x 256 outputs above) ->
+ * INVALID_CONFIG; else as qtip_moe_route. */
 qtip_status qtip_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int32_t m, const uint8_t* w_codes,
                            const uint8_t* w_scales, int32_t n, int32_t k, void* out, int32_t out_dtype, void* stream);
 
@@ -497,10 +502,10 @@ typedef struct qtip_mx_weights {
  * with expert e's matrices for the pairs sorted_pair[offsets[e]] .. sorted_pair[offsets[e + 1] - 1], fp32
  * accumulation, out bf16 or fp32 (out_dtype).  Rows of out whose pair is in no bin are not written.
  * Offsets outside [0, n k] are held to it and pair ids outside [0, n k) skipped, so device-side garbage
- * cannot reach memory out of bounds.  Only the pass's own weights are read; the others may be NULL.
- * Codes and out 16-byte aligned, scales 4-byte aligned; the plan gives E, k, H, I and max_tokens; its
- * rung, arm and variant do not matter.  Errors as qtip_moe_forward; a bad pass or out_dtype ->
- * INVALID_ARG. */
+ * cannot reach memory out of bounds; of a pair that two bins name either's row remains.  Only the
+ * pass's own weights are read; the others may be NULL.  Codes and out 16-byte aligned, scales 4-byte
+ * aligned; the plan gives E, k, H, I and max_tokens; its rung, arm and variant do not matter.  Errors
+ * as qtip_moe_forward; a bad pass or out_dtype -> INVALID_ARG. */
 enum { QTIP_MX_PASS_GATE_UP = 0, QTIP_MX_PASS_DOWN = 1 };
 qtip_status qtip_mx_expert_matmul(qtip_moe_plan_t plan, int32_t pass, const qtip_mx_weights* w /*host struct*/,
                                   const uint8_t* a_codes, const uint8_t* a_scales, const int32_t* offsets,
@@ -511,7 +516,8 @@ qtip_status qtip_mx_expert_matmul(qtip_moe_plan_t plan, int32_t pass, const qtip
  * quantise x, gate+up, quantise h, down, combine.  x is quantised by the nearest rule, h is rounded to
  * bf16 and quantised by the nearest rule; y = h Wd^T in fp32; out[t] = sum_j w[t,j] y(t, j) in fp32, j
  * ascending, cast to the plan's out_dtype.  Left-out slots add nothing.  workspace:
- * qtip_mx_moe_workspace_bytes(plan) bytes, 256-byte aligned, contents need no initialisation.
+ * qtip_mx_moe_workspace_bytes(plan) bytes, 256-byte aligned, contents need no initialisation; two
+ * calls, or replays of two captured graphs, that may overlap need one each.
  * Errors as qtip_moe_forward; a bad gate -> INVALID_ARG. */
 size_t qtip_mx_moe_workspace_bytes(qtip_moe_plan_t plan);
 qtip_status qtip_mx_moe_forward(qtip_moe_plan_t plan, const qtip_mx_weights* w /*host struct of device ptrs*/,

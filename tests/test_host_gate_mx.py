@@ -96,6 +96,16 @@ def test_matmul_refusals():
     assert call(m=1 << 20, n=1 << 20, k=32) == ARG
 
 
+def test_launches_past_2_32_threads_are_refused():
+    # four threads a block of 32 values; 256 threads for 16 weight rows; 512 for 256 x 256 outputs
+    quantize = lambda rows, cols: q.raw_status("qtip_mx_quantize", 256, q.QTIP_MX_SRC_BF16, rows, cols, cols,
+                                               q.QTIP_MX_SCALE_FLOOR, 256, 256, None, None)
+    assert quantize(1 << 30, 32) == ARG and quantize((1 << 30) - 63, 32) == ARG and quantize(1 << 20, 1 << 15) == ARG
+    matmul = lambda m, n: q.raw_status("qtip_mx_matmul", 256, 256, m, 256, 256, n, 32, 256, q.QTIP_OUT_F32, None)
+    assert matmul(1, 1 << 28) == CONFIG and matmul(16, (1 << 28) - 15) == CONFIG
+    assert matmul(1 << 19, (1 << 21) - 256) == CONFIG and "threads" in q.last_error_detail()
+
+
 def test_expert_matmul_and_layer_refusals(plan):
     w = q.make_mx_weights(*[256] * 6)
 

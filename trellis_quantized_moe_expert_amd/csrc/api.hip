@@ -1428,8 +1428,9 @@ qtip_status qtip_mx_quantize(const void* src, int32_t src_type, int32_t rows, in
     return fail(QTIP_ERR_INVALID_ARG, "unknown scale_rule");
   if (rows < 1 || cols < 1) return fail(QTIP_ERR_INVALID_CONFIG, "rows and cols must be >= 1 (an empty launch is an error)");
   if (row_stride < cols) return fail(QTIP_ERR_INVALID_ARG, "row_stride must be at least cols");
-  if ((int64_t)rows * (((int64_t)cols + kMxBlock - 1) / kMxBlock) >= ((int64_t)1 << 31))
-    return fail(QTIP_ERR_INVALID_ARG, "rows * blocks must be below 2^31");
+  // four threads a block, whole workgroups, below 2^32 threads
+  if ((int64_t)rows * (((int64_t)cols + kMxBlock - 1) / kMxBlock) > ((int64_t)1 << 30) - 64)
+    return fail(QTIP_ERR_INVALID_ARG, "rows * blocks must be at most 2^30 - 64");
   if (row_stride >= ((int64_t)1 << 40)) return fail(QTIP_ERR_INVALID_ARG, "row_stride must be below 2^40");
   if ((reinterpret_cast<uintptr_t>(src) & (src_type == QTIP_MX_SRC_F32 ? 3 : 1)) ||
       (reinterpret_cast<uintptr_t>(codes) & 15) || (reinterpret_cast<uintptr_t>(values) & 15))
@@ -1464,10 +1465,6 @@ qtip_status qtip_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int3
     return fail(QTIP_ERR_INVALID_ARG, "m * k and n * k must be below 2^37, m * n below 2^40");
   if (!mx_aligned(a_codes, a_scales) || !mx_aligned(w_codes, w_scales) || (reinterpret_cast<uintptr_t>(out) & 15))
     return fail(QTIP_ERR_INVALID_ARG, "codes and out must be 16-byte aligned, scales 4-byte aligned");
-  const hipStream_t st = (hipStream_t)stream;
-  int dev = 0;
-  const qtip_status s = ensure_current(st, &dev);
-  if (s != QTIP_OK) return s;
   MxMatmulParams p{};
   p.a = a_codes;
   p.a_scale = a_scales;
@@ -1481,6 +1478,11 @@ qtip_status qtip_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int3
   p.blocks = k / kMxBlock;
   p.out = out;
   p.out_bf16 = out_dtype == QTIP_OUT_BF16;
+  if (!mx_matmul_fits(p)) return fail(QTIP_ERR_INVALID_CONFIG, "m and n need a launch of 2^32 threads or more");
+  const hipStream_t st = (hipStream_t)stream;
+  int dev = 0;
+  const qtip_status s = ensure_current(st, &dev);
+  if (s != QTIP_OK) return s;
   const hipError_t e = launch_mx_matmul(p, st);
   return e == hipSuccess ? QTIP_OK : hip_fail(e, "MXFP4 matmul launch");
 }

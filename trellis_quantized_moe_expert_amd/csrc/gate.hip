@@ -23,14 +23,14 @@
 // neighbours of that order (the best one left among them) are equal in fp32, the wave chooses again
 // on the fp64 values.
 //
-// What bounds it: the issue of fp64 instructions, not memory.  16384 tokens of 256 experts, 8 of 8
-// groups' best 4, sigmoid with bias (16.8 MB of logits, 3.9 us at the copy rate) take 20.6 us in the
-// gate and 9.0 in placing, where each of 256 blocks adds up all blocks' counts out of L2; 27.7 for the
-// call.  A wave of four tokens issues about 700 fp64 instructions, half of them in the 256 sigmoids,
-// half in the sort and the merges, at 6.5 to 7 cycles each.  With the constants and lane masks of a
-// loop over tokens kept in vector registers the kernel spilled and took 25.  Small batches are bound by
-// launches and the latency of a chain of dependent steps: a token of 8 in one workgroup 7.3, 683 tokens
-// 5.6 and 7.5.
+// What bounds it: the issue of fp64 instructions, not memory.  16384 tokens of 256 experts, 8 choices
+// from the best 4 of 8 groups, sigmoid with bias (16.8 MB of logits, 3.9 us at the copy rate) take 21 us
+// in the gate and 9 in placing, where each of 256 workgroups adds up all blocks' counts out of L2; 28 for
+// the call.  A wave of four tokens issues 1860 vector instructions, about 700 of them fp64 (half for the
+// 16 sigmoids of a lane, half for the sort and the merges) at 6.5 to 7 cycles each.  With the constants
+// and lane masks of a loop over tokens kept in vector registers the kernel spilled and took 25.  Small
+// batches are bound by launches and the latency of a chain of dependent steps: a token of 8 choices,
+// routed and binned by one workgroup, 7; 683 tokens of 5 5.5 and 7.5.
 #include "mx_internal.h"
 #include "qtip_internal.h"
 
@@ -487,7 +487,7 @@ __device__ inline void peers_of(int e, int bits, int& rank, int& group) {
 
 // Places pairs [p0, p0 + count) (ids from `ids`, indexed by pair) of block b of `blocks`; hist NULL:
 // there is one block, and its counts are counted here.  Run by 1024 threads.  BATCH: times 64 pairs of a
-// wave whose ids are asked for before the first is used (683 tokens of 6 pairs by one workgroup: 7.6 us
+// wave whose ids are asked for before the first is used (683 tokens of 5 pairs by one workgroup: 7.6 us
 // with 8, 8.6 with 1; a token of 8, which has one load a wave anyway: 7.3 with 1, 7.7 with 8).
 template <int BATCH>
 __device__ __attribute__((always_inline)) inline void bin_block(const GateBins& o, const int32_t* ids, int E, int p0,

@@ -88,4 +88,7 @@ struct MxMatmulParams {
 
 hipError_t launch_mx_matmul(const MxMatmulParams& p, hipStream_t stream);
 
+// Whether the product's threads are few enough for a launch (a plan's expert passes always fit).
+bool mx_matmul_fits(const MxMatmulParams& p);
+
 }  // namespace qtip

@@ -20,6 +20,8 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
+constexpr int64_t kMostThreads = UINT32_MAX;  // of a launch
+
 constexpr int kFp4 = 4;  // the operand format of the f8f6f4 instructions: e2m1
 
 template <int SEL>
@@ -148,7 +150,9 @@ __device__ inline void tile_of_block(const MxMatmulParams& p, int tiles, int row
 // One workgroup: 16 weight rows (of both matrices where there are two) by MB * 16 activation rows;
 // its W waves split the inputs, run by run of 512, and add their sums through LDS.  Operands go from
 // memory to registers: with few activation rows a call is a stream of weights, and the more of them
-// are asked for at once the better.
+// are asked for at once the better.  Bound by those loads: 6 pairs of a 4096 x 2048 gate+up pass, 53.5 MB
+// of weights, 12.7 to 13.8 us (4.2 TB/s; 11.3 at the copy rate); 1 x 4096 x 4096, 8.9 MB, 4.0 us, of which
+// about 2 are the launch.
 // TAIL: the rows do not end with a run.
 template <int MB, int HALVES, int W, bool TAIL>
 __global__ __launch_bounds__(W * 64, MB * HALVES == 1 ? 6 : MB * HALVES == 2 ? 5 : 2) void direct_kernel(
@@ -263,12 +267,13 @@ __global__ __launch_bounds__(W * 64, MB * HALVES == 1 ? 6 : MB * HALVES == 2 ? 5
 }
 
 template <int MB, int HALVES, int W>
-hipError_t launch_direct(const MxMatmulParams& p, hipStream_t stream) {
+hipError_t launch_direct(const MxMatmulParams& p, hipStream_t stream, bool launch) {
   int64_t tiles = (p.m + MB * 16 - 1) / (MB * 16);
   // an expert's last tile may be partly filled: at most one more per expert that has pairs
   if (p.offsets) tiles = p.m / (MB * 16) + (p.m < p.E ? p.m : p.E);
   const int64_t grid = tiles * ((p.n + 15) / 16);
-  if (grid >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
+  if (grid * (W * 64) > kMostThreads) return hipErrorInvalidConfiguration;
+  if (!launch) return hipSuccess;
   if (p.blocks % 16 == 0)
     hipLaunchKernelGGL((direct_kernel<MB, HALVES, W, false>), dim3((unsigned)grid), dim3(W * 64), 0, stream, p);
   else
@@ -286,6 +291,17 @@ hipError_t launch_direct(const MxMatmulParams& p, hipStream_t stream) {
 // Instruction st of a stage takes block KS g + st of lane group g.  A row's 16-byte blocks are
 // stored so that the 16 lanes of an LDS read phase (rows 0-3, 12-15 of one lane group and rows 4-11
 // of the next, or the other way round) touch 16 different 16-byte columns of the banks: see place_of.
+//
+// What bounds it.  8192 x 8192 x 8192 in 256 x 256 tiles: 286 us with operands out of HBM, 270 with them
+// in the last-level cache, 3.8 and 4.1 PFLOP/s (a library's MXFP4 product reaches 2.9, the instruction
+// alone 7.1 on random data): the matrix instructions are busy 46 % of the time, the rest is a stage's
+// wait and barrier with one workgroup of 8 waves a CU.  Wider fragments a wave, loads of the next
+// fragments issued earlier, two wave groups a half stage apart and a raised wave priority were measured
+// and changed nothing or cost registers and time.  1024 tokens of a 256-expert, top-6 layer of 4096 x 2048,
+// gate+up, 32 x 128 tiles: the weights' bytes, 2.3 GB in 455 to 465 us (5.0 TB/s); 32 tokens, down: 351 MB
+// in 72 to 74 (4.8 TB/s).  8192 tokens, down, 192 pairs an expert in 256-row tiles: 461, 3.5 TB/s; a
+// quarter of each tile's rows is empty, and a workgroup finds its tile and fills its stages before the
+// first of only 16.
 //
 // Scales take the way through registers, 16 blocks (a window: four instructions) at a time,
 // double-buffered.  A lane group's four bytes go side by side, so that a fragment's scales of a
@@ -616,12 +632,13 @@ __global__ __launch_bounds__(WM * WN * 64) void tiled_kernel(MxMatmulParams p, i
 }
 
 template <int BM, int BN, int WM, int WN, int NST, int KS, int HALVES>
-hipError_t launch_tiled(const MxMatmulParams& p, hipStream_t stream) {
+hipError_t launch_tiled(const MxMatmulParams& p, hipStream_t stream, bool launch) {
   int64_t tiles = (p.m + BM - 1) / BM;
   if (p.offsets) tiles = p.m / BM + (p.m < p.E ? p.m : p.E);
   const int64_t row_blocks = (p.n + BN / HALVES - 1) / (BN / HALVES);
   const int64_t grid = (tiles + kXcds - 1) / kXcds * kXcds * row_blocks;
-  if (grid >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
+  if (grid * (WM * WN * 64) > kMostThreads) return hipErrorInvalidConfiguration;
+  if (!launch) return hipSuccess;
   hipLaunchKernelGGL((tiled_kernel<BM, BN, WM, WN, NST, KS, HALVES>), dim3((unsigned)grid), dim3(WM * WN * 64), 0, stream,
                      p, (int)tiles, (int)row_blocks);
   return hipGetLastError();
@@ -642,34 +659,39 @@ hipError_t launch_tiled(const MxMatmulParams& p, hipStream_t stream) {
 //     of 32 x 128        128 x 2048 x 4096 (64) 7.7, 8.2; 128 x 8192 x 2048 (256) 7.3, 6.7
 //   experts              6 pairs direct 13.5, 32 x 128 15.8; 12 pairs 21.2, 20.0; 24 pairs an expert 32 x 128 458,
 //                        128 x 128 485; 48 pairs 588, 533; 96 pairs 128 x 128 565, 256 x 256 659; 192 pairs 1050, 752
+// Without `launch` it says whether the launch could be made.
 template <int HALVES>
-hipError_t launch_halves(const MxMatmulParams& p, hipStream_t stream) {
+hipError_t launch_halves(const MxMatmulParams& p, hipStream_t stream, bool launch) {
   // the tiled kernel reads 16 scales at a time and addresses a tile's rows by 31-bit offsets
   const bool tiles = (int64_t)p.a_rows * p.blocks >= 16 && (int64_t)p.E * p.n * p.blocks >= 16 && p.blocks < 1 << 18;
   const int64_t row_blocks = (p.n + 15) / 16;
   const bool few = p.offsets ? p.m <= 8 || (p.m <= 16 && p.m * row_blocks <= 1280) : p.m <= 16;
-  if (few && !p.offsets && p.blocks >= 128) return launch_direct<1, HALVES, 8>(p, stream);
-  if (few) return launch_direct<1, HALVES, 4>(p, stream);
-  if (!tiles || (!p.offsets && p.m <= 64 && p.n <= 4096)) return launch_direct<2, HALVES, 4>(p, stream);
+  if (few && !p.offsets && p.blocks >= 128) return launch_direct<1, HALVES, 8>(p, stream, launch);
+  if (few) return launch_direct<1, HALVES, 4>(p, stream, launch);
+  if (!tiles || (!p.offsets && p.m <= 64 && p.n <= 4096)) return launch_direct<2, HALVES, 4>(p, stream, launch);
   if (p.offsets) {
     const int fill = (p.m + p.E - 1) / p.E;  // pairs an expert gets on average
-    if (fill <= 28) return launch_tiled<32, 128, 1, 4, 2, 2, HALVES>(p, stream);
-    if (fill <= 160) return launch_tiled<128, 128, 2, 2, 4, 1, HALVES>(p, stream);
-    return launch_tiled<256, 256, 2, 4, 4, 1, HALVES>(p, stream);
+    if (fill <= 28) return launch_tiled<32, 128, 1, 4, 2, 2, HALVES>(p, stream, launch);
+    if (fill <= 160) return launch_tiled<128, 128, 2, 2, 4, 1, HALVES>(p, stream, launch);
+    return launch_tiled<256, 256, 2, 4, 4, 1, HALVES>(p, stream, launch);
   }
   auto groups = [&](int64_t bm, int64_t bn) { return (p.m + bm - 1) / bm * ((p.n + bn - 1) / bn); };
-  if (groups(256, 256) >= 256) return launch_tiled<256, 256, 2, 4, 4, 1, HALVES>(p, stream);
-  if (groups(128, 128) >= 200) return launch_tiled<128, 128, 2, 2, 2, 2, HALVES>(p, stream);
-  if (groups(64, 128) >= 256) return launch_tiled<64, 128, 1, 4, 2, 2, HALVES>(p, stream);
-  if (groups(32, 128) > 256) return launch_tiled<32, 128, 1, 4, 2, 2, HALVES>(p, stream);
-  if (groups(32, 128) >= 128) return launch_tiled<32, 128, 1, 4, 4, 2, HALVES>(p, stream);
-  return launch_tiled<32, 64, 1, 2, 4, 2, HALVES>(p, stream);
+  if (groups(256, 256) >= 256) return launch_tiled<256, 256, 2, 4, 4, 1, HALVES>(p, stream, launch);
+  if (groups(128, 128) >= 200) return launch_tiled<128, 128, 2, 2, 2, 2, HALVES>(p, stream, launch);
+  if (groups(64, 128) >= 256) return launch_tiled<64, 128, 1, 4, 2, 2, HALVES>(p, stream, launch);
+  if (groups(32, 128) > 256) return launch_tiled<32, 128, 1, 4, 2, 2, HALVES>(p, stream, launch);
+  if (groups(32, 128) >= 128) return launch_tiled<32, 128, 1, 4, 4, 2, HALVES>(p, stream, launch);
+  return launch_tiled<32, 64, 1, 2, 4, 2, HALVES>(p, stream, launch);
 }
 
 }  // namespace
 
 hipError_t launch_mx_matmul(const MxMatmulParams& p, hipStream_t stream) {
-  return p.w1 ? launch_halves<2>(p, stream) : launch_halves<1>(p, stream);
+  return p.w1 ? launch_halves<2>(p, stream, true) : launch_halves<1>(p, stream, true);
+}
+
+bool mx_matmul_fits(const MxMatmulParams& p) {
+  return (p.w1 ? launch_halves<2>(p, nullptr, false) : launch_halves<1>(p, nullptr, false)) == hipSuccess;
 }
 
 }  // namespace qtip

