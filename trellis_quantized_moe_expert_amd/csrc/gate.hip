@@ -30,7 +30,7 @@
 // 16 sigmoids of a lane, half for the sort and the merges) at 6.5 to 7 cycles each.  With the constants
 // and lane masks of a loop over tokens kept in vector registers the kernel spilled and took 25.  Small
 // batches are bound by launches and the latency of a chain of dependent steps: a token of 8 choices,
-// routed and binned by one workgroup, 7; 683 tokens of 5 5.5 and 7.5.
+// routed and binned by one workgroup, 7; 683 tokens of 5 choices 5.5 and 7.
 #include "mx_internal.h"
 #include "qtip_internal.h"
 
@@ -487,8 +487,9 @@ __device__ inline void peers_of(int e, int bits, int& rank, int& group) {
 
 // Places pairs [p0, p0 + count) (ids from `ids`, indexed by pair) of block b of `blocks`; hist NULL:
 // there is one block, and its counts are counted here.  Run by 1024 threads.  BATCH: times 64 pairs of a
-// wave whose ids are asked for before the first is used (683 tokens of 5 pairs by one workgroup: 7.6 us
-// with 8, 8.6 with 1; a token of 8, which has one load a wave anyway: 7.3 with 1, 7.7 with 8).
+// wave whose ids are asked for before the first is used, and the first of which are kept for the second
+// walk (683 tokens of 5 pairs by one workgroup: 7.0 us with 8, 7.6 where the second walk reads them
+// again, 8.6 with 1; a token of 8, which has one load a wave anyway: 7.3 with 1, 7.7 with 8).
 template <int BATCH>
 __device__ __attribute__((always_inline)) inline void bin_block(const GateBins& o, const int32_t* ids, int E, int p0,
                                                                 int count, const int32_t* hist, int blocks, int b,
@@ -496,23 +497,32 @@ __device__ __attribute__((always_inline)) inline void bin_block(const GateBins& 
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   int bits = 1;
   while ((1 << bits) <= E) ++bits;
-  for (int e = lane; e < E; e += 64) s.wave_cnt[wv][e] = 0;
-  for (int e = tid; e < E; e += 1024) s.total[e] = s.before[e] = 0;
   const int chunk = ((count + kGateWaves - 1) / kGateWaves + 63) & ~63;
   const int lo = wv * chunk, hi = min(count, lo + chunk);
+  auto load = [&](int i0, int (&id)[BATCH]) {
+#pragma unroll
+    for (int r = 0; r < BATCH; ++r) {
+      const int i = i0 + 64 * r + lane;
+      id[r] = ids[p0 + min(i, hi - 1)];
+      id[r] = i < hi && id[r] >= 0 && id[r] < E ? id[r] : E;
+    }
+  };
+  int first[BATCH];  // kept for the second walk
+  if (lo < hi) load(lo, first);
+  for (int e = lane; e < E; e += 64) s.wave_cnt[wv][e] = 0;
+  for (int e = tid; e < E; e += 1024) s.total[e] = s.before[e] = 0;
   // the wave's pairs in order, 64 at a time: step(place, expert or E)
   auto each = [&](auto step) {
-    for (int i0 = lo; i0 < hi; i0 += 64 * BATCH) {
-      int id[BATCH];
-#pragma unroll
-      for (int r = 0; r < BATCH; ++r) {
-        const int i = i0 + 64 * r + lane;
-        id[r] = ids[p0 + min(i, hi - 1)];
-        id[r] = i < hi && id[r] >= 0 && id[r] < E ? id[r] : E;
-      }
+    auto walk = [&](int i0, const int (&id)[BATCH]) {
 #pragma unroll
       for (int r = 0; r < BATCH; ++r)
         if (i0 + 64 * r < hi) step(i0 + 64 * r + lane, id[r]);
+    };
+    if (lo < hi) walk(lo, first);
+    for (int i0 = lo + 64 * BATCH; i0 < hi; i0 += 64 * BATCH) {
+      int id[BATCH];
+      load(i0, id);
+      walk(i0, id);
     }
   };
   each([&](int, int e) {
