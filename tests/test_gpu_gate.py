@@ -196,6 +196,22 @@ def test_skewed_batch_fills_one_bin():
     run(logits, 16, 2, None, score="sigmoid")
 
 
+def test_blocks_of_more_pairs_than_a_wave_keeps():
+    # 512 blocks of 320 tokens, 640 pairs a wave; the oracle chooses for the 700 different rows
+    import torch
+    n, E, k = 140000, 64, 32
+    rng = np.random.default_rng(11)
+    rows = rng.standard_normal((700, E)).astype(np.float32)
+    rows[::7, rng.permutation(E)[:40]] = -np.inf                # 24 experts left: slots stay empty
+    say(f"gate n={n} E={E} k={k}, many pairs a block")
+    r = Route(E, k, n, score="sigmoid", tiles=False)
+    r.call(torch.from_numpy(rows).cuda().repeat(n // 700, 1))
+    got = r.host()
+    r.close()
+    idx, w = oracle.route(rows, None, k, score="sigmoid")
+    check(got, np.tile(idx, (n // 700, 1)), np.tile(w, (n // 700, 1)), E, n, k)
+
+
 def test_gate_in_a_graph_and_on_another_stream():
     import torch
     rng = np.random.default_rng(8)

@@ -153,6 +153,22 @@ def test_product_one_block_at_a_time():
         assert np.array_equal(got, values(*a) @ values(*w).T), b   # 32 products: exact in fp32
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 200, 160), (40, 300, 544), (300, 2050, 96), (1000, 2056, 160),
+                                   (1030, 3200, 96), (4000, 4100, 64)])
+def test_a_nan_block_reaches_its_own_outputs_only(m, n, k):
+    say(f"product {m}x{n}x{k} with NaN blocks")
+    rng = np.random.default_rng(m + n)
+    a, w = packed(rng, m, k), packed(rng, n, k)
+    before = product(a, w, "fp32")
+    a[1][m - 1, -1] = 255                 # the last block of the last row
+    w[1][n - 1, -1] = w[1][n // 2, 0] = 255
+    after = product(a, w, "fp32")
+    hit = np.zeros((m, n), bool)
+    hit[m - 1] = hit[:, n - 1] = hit[:, n // 2] = True
+    assert np.all(np.isnan(after[hit]))
+    assert np.array_equal(after[~hit], before[~hit])
+
+
 def test_product_scale_extremes_and_nan_blocks():
     say("product scale extremes")
     rng = np.random.default_rng(6)
