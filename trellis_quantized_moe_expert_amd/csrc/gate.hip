@@ -17,7 +17,7 @@
 //
 // The choice is the one that fp64 makes: two experts' c_e can lie closer together than fp32
 // resolves (the scores of a sigmoid crowd together, the bias is added on top).  Scores and groups
-// are fp64 throughout (vector fp64 runs at fp32's rate here).  The choice itself runs on c_e rounded
+// are fp64 throughout (a vector fp64 instruction takes 6.5 to 7 cycles).  The choice runs on c_e rounded
 // to fp32, which keeps every order that it does not make equal: each lane sorts its experts, and
 // pairs of lanes merge their best KL until all lanes hold the token's best KL in order.  Where two
 // neighbours of that order (the best one left among them) are equal in fp32, the wave chooses again
@@ -27,7 +27,7 @@
 // from the best 4 of 8 groups, sigmoid with bias (16.8 MB of logits, 3.9 us at the copy rate) take 21 us
 // in the gate and 9 in placing, where each of 256 workgroups adds up all blocks' counts out of L2; 28 for
 // the call.  A wave of four tokens issues 1860 vector instructions, about 700 of them fp64 (half for the
-// 16 sigmoids of a lane, half for the sort and the merges) at 6.5 to 7 cycles each.  With the constants
+// 16 sigmoids of a lane, half for the sort and the merges).  With the constants
 // and lane masks of a loop over tokens kept in vector registers the kernel spilled and took 25.  Small
 // batches are bound by launches and the latency of a chain of dependent steps: a token of 8 choices,
 // routed and binned by one workgroup, 7; 683 tokens of 5 choices 5.5 and 7.
@@ -108,8 +108,8 @@ struct ExpTerms {
   }
 };
 
-// exp(x), -1100 <= x <= 700, to about one unit in the last place: x = k ln 2 + r, |r| <= ln 2 / 2, ln 2 in two parts, and the Taylor polynomial of exp(r) up to
-// r^13 / 13! (the next term is under 2^-57).
+// exp(x), -1100 <= x <= 700, to about one unit in the last place: x = k ln 2 + r, |r| <= ln 2 / 2, ln 2 in
+// two parts, and the Taylor polynomial of exp(r) up to r^13 / 13! (the next term is under 2^-57).
 __device__ inline double exp_f64(double x, const ExpTerms& m) {
   const double k = rint(x * m.log2e);
   double r = fma(k, m.ln2_hi, x);
@@ -313,7 +313,8 @@ __device__ inline void load_four(__amdgpu_buffer_rsrc_t r, int at, float (&v)[Q]
 }
 
 // The fp64 values of the experts a lane holds, -inf for those not to be chosen (their groups among
-// them); e0: its first expert.  Its token's logits are at byte `at` of `logits`.  top, inv: a softmax's largest logit and 1 / sum.
+// them); e0: its first expert.  Its token's logits are at byte `at` of `logits`.  top, inv: a softmax's
+// largest logit and 1 / sum.
 template <int LANES, int Q>
 __device__ __attribute__((always_inline)) inline void token_values(const GateParams& p, const GateShape& gs,
                                                                    __amdgpu_buffer_rsrc_t logits, int at, const ExpTerms& m,
@@ -380,7 +381,8 @@ __device__ __attribute__((noinline)) Ids<TURNS> choose_again(GateParams p, GateS
   Ids<TURNS> ids;
 #pragma unroll
   for (int i = 0; i < TURNS; ++i) ids.id[i] = -1;
-  token_values<LANES, Q>(p, gs, token_rows<LANES>(p, __builtin_amdgcn_readfirstlane(first)), at, ExpTerms(), e0, top, inv, c);
+  token_values<LANES, Q>(p, gs, token_rows<LANES>(p, __builtin_amdgcn_readfirstlane(first)), at, ExpTerms(), e0, top,
+                         inv, c);
   choose_exact<LANES, Q, TURNS>(p.k, c, e0, ids.id);
   return ids;
 }
