@@ -414,7 +414,9 @@ qtip_status qtip_expert_matmul(qtip_moe_plan_t plan, int32_t arm, const uint8_t*
  * never chosen (a bias of -inf takes an expert out); a +inf logit scores 1 (softmax: shared among
  * the +inf ones).  A slot that no expert is left for holds the id -1 and the weight 0, and its pair
  * is in no bin: offsets[E] then is less than n k and the places of sorted_pair past it are not
- * written.  If the chosen scores' sum is 0, renormalised weights are 0. */
+ * written.  Scores below exp(-745), where fp64 ends, count as 0 (a softmax's: logits more than 745 under
+ * the largest one, or behind a +inf one); if all of a token's chosen scores are 0, its renormalised
+ * weights are 0. */
 enum { QTIP_GATE_SOFTMAX = 0, QTIP_GATE_SIGMOID = 1 };
 typedef struct qtip_moe_gate {
   int32_t score;       /* QTIP_GATE_SOFTMAX or QTIP_GATE_SIGMOID */

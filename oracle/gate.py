@@ -13,8 +13,7 @@ import numpy as np
 def scores(row, score: str):
     """Scores of one token's logits; NaN logits score NaN, which is never chosen."""
     if score == "sigmoid":
-        return [1.0 / (1.0 + math.exp(-v)) if v >= 0 else math.exp(v) / (1.0 + math.exp(v)) if v > -700 else 0.0
-                for v in row]
+        return [1.0 / (1.0 + math.exp(-v)) if v >= 0 else math.exp(v) / (1.0 + math.exp(v)) for v in row]
     num = [v for v in row if not math.isnan(v)]
     top = max(num, default=-math.inf)
     if top == -math.inf:
@@ -23,6 +22,19 @@ def scores(row, score: str):
           for v in row]
     z = math.fsum(v for v in ex if not math.isnan(v))
     return [v / z for v in ex]
+
+
+def shares(chosen, w, top):
+    """The chosen scores w divided by their sum, from their logits where fp64 does not hold the scores:
+    both kinds then go like exp(logit).  top: a softmax's largest logit, a sigmoid's 0."""
+    z = math.fsum(w)
+    if z > 1e-250:
+        return [v / z for v in w]
+    largest = max(chosen, default=-math.inf)
+    if not largest - top >= -745.0:                # scores below exp(-745) count as 0
+        return [0.0] * len(w)
+    ex = [math.exp(v - largest) for v in chosen]
+    return [v / math.fsum(ex) for v in ex]
 
 
 def route_token(row, bias, k, score="softmax", num_groups=1, top_groups=1, group_top=1, renormalise=1, scale=1.0):
@@ -43,8 +55,8 @@ def route_token(row, bias, k, score="softmax", num_groups=1, top_groups=1, group
     idx = sorted((e for e in range(E) if able[e]), key=lambda e: (-c[e], e))[:k]
     w = [s[e] for e in idx]
     if renormalise:
-        z = math.fsum(w)
-        w = [v / z if z > 0 else 0.0 for v in w]
+        top = 0.0 if score == "sigmoid" else max((v for v in row if not math.isnan(v)), default=0.0)
+        w = shares([row[e] for e in idx], w, top)
     gap = k - len(idx)
     return idx + [-1] * gap, [v * scale for v in w] + [0.0] * gap
 

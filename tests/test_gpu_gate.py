@@ -174,6 +174,52 @@ def test_extreme_logits():
     run((logits * 20).astype(np.float32), 48, 4, (0.01 * rng.standard_normal(48)).astype(np.float32), score="softmax")
 
 
+# (E, k, groups, copies of the rows): one workgroup, a wave or a quarter of one a token, 4 to 32 experts a
+# lane, lists of 8 and of 32 (two choices a lane)
+LOW = [(48, 2, 1, 1), (48, 5, 4, 1), (48, 5, 4, 4), (240, 24, 1, 200), (256, 8, 8, 200), (300, 5, 2, 3),
+       (1000, 9, 1, 3)]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,copies", LOW)
+def test_weights_of_scores_at_the_end_of_fp64(E, k, groups, copies, score):
+    # the experts that can be chosen lie `gap` below the softmax's largest logit (a sigmoid: below 0); the
+    # bias takes the loud one out and makes the choice, the scores being far smaller
+    rng = np.random.default_rng(E + k)
+    gaps = [0, 300, 484, 486, 700, 702, 705, 708, 709, 712, 720, 735, 743, 746, 800, 2e5]
+    near = rng.uniform(-2.0, 0.0, (len(gaps), E)).astype(np.float32)
+    near[5] = 0.0                                      # equal scores
+    near[np.arange(len(gaps)), rng.integers(1, E, len(gaps))] = -np.inf
+    logits = (near - np.array(gaps, np.float32)[:, None]).astype(np.float32)
+    if score == "softmax":
+        logits += 90.0
+        logits[:, 0] = 90.0
+    bias = rng.permutation(E).astype(np.float32) / 64
+    bias[0] = -np.inf
+    say(f"gate low scores E={E} k={k} groups={groups} {score}")
+    for renorm in (1, 0):
+        run(np.tile(logits, (copies, 1)), E, k, bias, score=score, num_groups=groups, top_groups=max(1, groups // 2),
+            renormalise=renorm, scale=2.5)
+    lone = np.full((3, E), -np.inf, np.float32)        # one expert left, and none; the loud one infinite
+    lone[0, 0], lone[0, 3] = 0.0, -730.0
+    lone[1, 0] = 0.0
+    lone[2, 0], lone[2, 1:4] = np.inf, 5.0
+    run(lone, E, k, bias, score=score)
+
+
+@pytest.mark.parametrize("groups", [1, 4])
+def test_order_of_low_sigmoids(groups):
+    # scores of 4e-305 to 7e-308 are fp64 numbers: their order decides, among groups too
+    rng = np.random.default_rng(40 + groups)
+    E = 64
+    logits = (-701.0 - rng.permuted(np.tile(np.arange(E) * 0.1, (40, 1)), axis=1)).astype(np.float32)
+    say(f"gate order of low sigmoids, groups={groups}")
+    for n in (40, 5):
+        for group_top in (1, 2):
+            run(logits[:n], E, 6, None, score="sigmoid", num_groups=groups, top_groups=max(1, groups // 2),
+                group_top=group_top)
+
+
 def test_fewer_tokens_than_the_plan_and_rows_behind_left_alone():
     import torch
     rng = np.random.default_rng(2)

@@ -41,6 +41,19 @@ def test_masked_experts_are_never_chosen():
     assert idx == [0, 2, 1] and w == [0.5, 0.5, 0.0]
 
 
+def test_shares_of_scores_at_the_end_of_fp64():
+    # exp(-1) : 1 whatever lies above, down to scores of exp(-745)
+    want = [1 / (1 + math.exp(-1.0)), 1 / (1 + math.e)]
+    for gap in (0.0, 600.0, 709.0, 720.0, 744.0):
+        row, bias = [40.0, -gap + 40.0, -gap + 39.0], [-math.inf, 2.0, 1.0]
+        assert gate.route_token(row, bias, 2)[1] == pytest.approx(want, rel=1e-12)
+        assert gate.route_token([-gap - 5.0, -gap - 6.0], None, 2, "sigmoid")[1] == (
+            [0.0, 0.0] if gap > 740 else pytest.approx(want, rel=2e-2 if gap == 0 else 1e-12))
+    assert gate.route_token([40.0, -706.0, -706.0], [-math.inf, 0.0, 0.0], 2)[1] == [0.0, 0.0]
+    assert gate.route_token([math.inf, 3.0, 3.0], [-math.inf, 0.0, 0.0], 2)[1] == [0.0, 0.0]
+    assert gate.route_token([-703.0, -701.0, -702.0], None, 2, "sigmoid")[0] == [1, 2]
+
+
 def test_bins_leave_out_pairs_without_an_expert():
     counts, offsets, order = gate.bins(np.array([[2, 0], [-1, 2], [0, -1]]), 3)
     assert counts.tolist() == [2, 0, 2] and offsets.tolist() == [0, 2, 2, 4] and order.tolist() == [1, 4, 0, 3]

@@ -108,7 +108,7 @@ struct ExpTerms {
   }
 };
 
-// exp(x), -1100 <= x <= 700, to about one unit in the last place: x = k ln 2 + r, |r| <= ln 2 / 2, ln 2 in
+// exp(x), -1100 <= x <= 0, to about one unit in the last place: x = k ln 2 + r, |r| <= ln 2 / 2, ln 2 in
 // two parts, and the Taylor polynomial of exp(r) up to r^13 / 13! (the next term is under 2^-57).
 __device__ inline double exp_f64(double x, const ExpTerms& m) {
   const double k = rint(x * m.log2e);
@@ -123,17 +123,19 @@ __device__ inline double exp_f64(double x, const ExpTerms& m) {
   return ldexp(y, (int)k);
 }
 
-// 1 / d, d in [1, 2^1020]: the hardware's estimate and two Newton steps.
+// 1 / d, d in [1, 2048]: the hardware's estimate and two Newton steps.
 __device__ inline double recip_f64(double d) {
   double y = __builtin_amdgcn_rcp(d);
   y = fma(fma(-d, y, 1.0), y, y);
   return fma(fma(-d, y, 1.0), y, y);
 }
 
-// The sigmoid of a logit; 0 below -700, where exp(-l) nears the end of fp64's range, 1 from 700 on.
+// The sigmoid of a logit, from the exponential of its negative magnitude: nothing overflows, and low logits
+// keep their scores down to the end of fp64's range.
 __device__ inline double sigmoid_f64(float l, const ExpTerms& m) {
-  const double s = recip_f64(1.0 + exp_f64((double)fminf(fmaxf(-l, -700.0f), 700.0f), m));
-  return l < -700.0f ? 0.0 : s;
+  const double e = exp_f64((double)fmaxf(-fabsf(l), -1100.0f), m);
+  const double r = recip_f64(1.0 + e);
+  return l < 0.0f ? e * r : r;
 }
 
 // A logit's part of a softmax, 0 below exp(-1100).  l == top also where both are infinite: such logits
@@ -387,6 +389,40 @@ __device__ __attribute__((noinline)) Ids<TURNS> choose_again(GateParams p, GateS
   return ids;
 }
 
+template <int TURNS> struct Chosen { float logit[TURNS]; };
+template <int TURNS> struct Shares { double part[TURNS]; };
+
+// Below this sum of the chosen scores their quotients come from low_shares: 1 / sum could pass fp64's
+// range, and scores under 2^-1022 have lost bits.  (Above it a score of fewer than 52 bits has a share
+// under 2^-322, nothing in fp32 whatever the scale.)
+constexpr double kLowSum = 0x1p-700;
+
+// The chosen scores divided by their sum where that is below kLowSum, from the logits (-inf: none).  Both
+// scores then go like exp(l), so the largest chosen logit takes the place of the softmax's largest one.
+// If even its score, exp(largest - top) (a sigmoid: top = 0), is below exp(-745), all are 0.  A call of
+// its own, as choose_again: it is rarely needed.
+template <int LANES, int TURNS>
+__device__ __attribute__((noinline)) Shares<TURNS> low_shares(Chosen<TURNS> x, float top) {
+  const ExpTerms terms;
+  float largest = x.logit[0];
+#pragma unroll
+  for (int i = 1; i < TURNS; ++i) largest = fmaxf(largest, x.logit[i]);
+  largest = lanes_max<LANES>(largest);
+  const bool some = (double)largest - (double)top >= -745.0;  // false for -inf - -inf
+  Shares<TURNS> s;
+  double sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < TURNS; ++i) {
+    const double part = exp_f64(fmax((double)x.logit[i] - (double)largest, -1100.0), terms);
+    s.part[i] = some && x.logit[i] > -INFINITY ? part : 0.0;
+    sum += s.part[i];
+  }
+  sum = lanes_sum<LANES>(sum);
+#pragma unroll
+  for (int i = 0; i < TURNS; ++i) s.part[i] = some ? s.part[i] / sum : 0.0;
+  return s;
+}
+
 // Routes the wave's 64 / LANES tokens from token `first` on.  sel: their ids in LDS, k of each (NULL:
 // not wanted).
 template <int LANES, int Q, int KL>
@@ -420,17 +456,26 @@ __device__ __attribute__((always_inline)) inline void gate_tokens(const GatePara
   }
 
   // the weights, a choice a lane
+  Chosen<kTurns> x;
   double s[kTurns], z = 0.0;
 #pragma unroll
   for (int i = 0; i < kTurns; ++i) {
-    const float x = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(logits, at + 4 * max(id[i], 0), 0, 0));
-    const double part = p.sigmoid ? sigmoid_f64(x, terms) : softmax_part(x, top, terms) * inv;
+    x.logit[i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(logits, at + 4 * max(id[i], 0), 0, 0));
+    x.logit[i] = id[i] >= 0 ? x.logit[i] : -INFINITY;
+    const double part = p.sigmoid ? sigmoid_f64(x.logit[i], terms) : softmax_part(x.logit[i], top, terms) * inv;
     s[i] = id[i] >= 0 ? part : 0.0;
     z += s[i];
   }
   if (p.renormalise) {
     z = lanes_sum<LANES>(z);
-    z = z > 0.0 ? 1.0 / z : 0.0;
+    const bool low = z < kLowSum;
+    z = 1.0 / z;
+    if (__ballot(low)) {
+      const Shares<kTurns> shares = low_shares<LANES, kTurns>(x, p.sigmoid ? 0.0f : top);
+#pragma unroll
+      for (int i = 0; i < kTurns; ++i) s[i] = low ? shares.part[i] : s[i];
+      z = low ? 1.0 : z;
+    }
   } else {
     z = 1.0;
   }
