@@ -106,6 +106,15 @@ def test_launches_past_2_32_threads_are_refused():
     assert matmul(1 << 19, (1 << 21) - 256) == CONFIG and "threads" in q.last_error_detail()
 
 
+@pytest.mark.parametrize("m,n", [(1, 2 ** 31 - 16), (1, 2 ** 31 - 15), (1, 2 ** 31 - 1), (16, 2 ** 31 - 1),
+                                 (17, 2 ** 31 - 1), (300, 2 ** 31 - 130), (511, 2 ** 31 - 1), (2 ** 31 - 1, 1),
+                                 (2 ** 31 - 1, 16), (2 ** 31 - 255, 300), (2 ** 31 - 257, 511)])
+def test_products_of_rows_next_to_2_31_are_refused(m, n):
+    # the launch's arithmetic in 64 bits: in 32 these counts wrap to a negative grid
+    status = q.raw_status("qtip_mx_matmul", 256, 256, m, 256, 256, n, 32, 256, q.QTIP_OUT_F32, None)
+    assert status == CONFIG and "threads" in q.last_error_detail()
+
+
 def test_expert_matmul_and_layer_refusals(plan):
     w = q.make_mx_weights(*[256] * 6)
 

@@ -268,10 +268,10 @@ __global__ __launch_bounds__(W * 64, MB * HALVES == 1 ? 6 : MB * HALVES == 2 ? 5
 
 template <int MB, int HALVES, int W>
 hipError_t launch_direct(const MxMatmulParams& p, hipStream_t stream, bool launch) {
-  int64_t tiles = (p.m + MB * 16 - 1) / (MB * 16);
+  int64_t tiles = ((int64_t)p.m + MB * 16 - 1) / (MB * 16);  // 64 bits: m and n go up to 2^31 - 1
   // an expert's last tile may be partly filled: at most one more per expert that has pairs
   if (p.offsets) tiles = p.m / (MB * 16) + (p.m < p.E ? p.m : p.E);
-  const int64_t grid = tiles * ((p.n + 15) / 16);
+  const int64_t grid = tiles * (((int64_t)p.n + 15) / 16);
   if (grid * (W * 64) > kMostThreads) return hipErrorInvalidConfiguration;
   if (!launch) return hipSuccess;
   if (p.blocks % 16 == 0)
@@ -633,9 +633,9 @@ __global__ __launch_bounds__(WM * WN * 64) void tiled_kernel(MxMatmulParams p, i
 
 template <int BM, int BN, int WM, int WN, int NST, int KS, int HALVES>
 hipError_t launch_tiled(const MxMatmulParams& p, hipStream_t stream, bool launch) {
-  int64_t tiles = (p.m + BM - 1) / BM;
+  int64_t tiles = ((int64_t)p.m + BM - 1) / BM;
   if (p.offsets) tiles = p.m / BM + (p.m < p.E ? p.m : p.E);
-  const int64_t row_blocks = (p.n + BN / HALVES - 1) / (BN / HALVES);
+  const int64_t row_blocks = ((int64_t)p.n + BN / HALVES - 1) / (BN / HALVES);
   const int64_t grid = (tiles + kXcds - 1) / kXcds * kXcds * row_blocks;
   if (grid * (WM * WN * 64) > kMostThreads) return hipErrorInvalidConfiguration;
   if (!launch) return hipSuccess;
@@ -664,7 +664,7 @@ template <int HALVES>
 hipError_t launch_halves(const MxMatmulParams& p, hipStream_t stream, bool launch) {
   // the tiled kernel reads 16 scales at a time and addresses a tile's rows by 31-bit offsets
   const bool tiles = (int64_t)p.a_rows * p.blocks >= 16 && (int64_t)p.E * p.n * p.blocks >= 16 && p.blocks < 1 << 18;
-  const int64_t row_blocks = (p.n + 15) / 16;
+  const int64_t row_blocks = ((int64_t)p.n + 15) / 16;
   const bool few = p.offsets ? p.m <= 8 || (p.m <= 16 && p.m * row_blocks <= 1280) : p.m <= 16;
   if (few && !p.offsets && p.blocks >= 128) return launch_direct<1, HALVES, 8>(p, stream, launch);
   if (few) return launch_direct<1, HALVES, 4>(p, stream, launch);
