@@ -59,6 +59,33 @@ def test_quantise_matches_the_oracle(rows, cols, pad, kind, rule):
     check_quantise(wide.to(dtype_of(kind)).cuda()[:, :cols], kind, rule, with_values=cols != 256)
 
 
+@pytest.mark.parametrize("cols", [2 ** 31 - 1, 2 ** 31 - 9])
+def test_quantise_one_row_of_all_columns_there_can_be(cols):
+    # 2^14 values over and over; the last block is not full, its last eight values the last of 31-bit columns
+    import torch
+    say(f"quantise 1x{cols}")
+    part = 2 ** 14
+    base = torch.randn(1, part, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    ref = mx.quantise(base.double().numpy(), "nearest")
+    x = base.cuda().repeat(1, 2 ** 31 // part)[:, :cols]
+    codes = torch.full((1, 2 ** 30), 0xA5, dtype=torch.uint8, device="cuda:0")
+    scales = torch.full((1, 2 ** 26), 0xA5, dtype=torch.uint8, device="cuda:0")
+    vals = torch.full((2 ** 31,), -7.0, dtype=torch.bfloat16, device="cuda:0")
+    q.qtip_mx_quantize(x, SRC["bf16"], 1, cols, cols, RULE["nearest"], codes, scales, vals)
+    torch.cuda.synchronize()
+    whole = cols // part                                   # repetitions before the last, shorter one
+    for got, want in zip((codes[0], scales[0], vals), ref):
+        rows = got.view(-1, want.shape[1])
+        want = torch.from_numpy(want).to(got.dtype).cuda()
+        assert all(bool((piece == want).all()) for piece in rows[:whole].split(2 ** 13))
+    rest = cols - whole * part
+    tail = mx.quantise(base[:, :rest].double().numpy(), "nearest")
+    assert np.array_equal(codes[0, whole * part // 2:].cpu().numpy()[:tail[0].shape[1]], tail[0][0])
+    assert np.array_equal(scales[0, whole * part // 32:].cpu().numpy()[:tail[1].shape[1]], tail[1][0])
+    assert np.array_equal(vals[whole * part:cols].double().cpu().numpy(), tail[2][0])
+    assert bool((vals[cols:] == -7.0).all())
+
+
 @pytest.mark.parametrize("rule", ["floor", "nearest"])
 @pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
 def test_quantise_borders_and_extremes(kind, rule):

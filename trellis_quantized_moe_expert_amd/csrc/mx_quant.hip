@@ -94,16 +94,17 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(MxQuantParams p
   typedef typename T::Elem Elem;
   constexpr int kWords = T::kWords;
   struct __attribute__((packed, aligned(sizeof(Elem)))) Eight { uint32_t w[kWords]; };  // at any element's address
-  const uint32_t blocks = (uint32_t)(p.cols + kMxBlock - 1) / kMxBlock;
+  const uint32_t blocks = ((uint32_t)p.cols + kMxBlock - 1) / kMxBlock;
   const int64_t item = (int64_t)blockIdx.x * kQuantThreads + threadIdx.x;
-  const uint32_t block = (uint32_t)(item >> 2);  // rows x blocks < 2^31
+  const uint32_t block = (uint32_t)(item >> 2);  // rows x blocks < 2^30
   if (block >= blocks * (uint32_t)p.rows) return;  // a block's four threads leave together
   const uint32_t row = block / blocks;
   const int part = (int)((block - row * blocks) * 4) + (int)(item & 3);
-  const int c0 = part * kPerThread;
+  const int c0 = part * kPerThread;  // at most 2^31 - 8
+  const int left = p.cols - c0;      // of the row, these eight and what follows; below 0 past its end
   const Elem* src = reinterpret_cast<const Elem*>(p.src) + (int64_t)row * p.row_stride + c0;
   uint32_t w[kWords];
-  if (c0 + kPerThread <= p.cols) {
+  if (left >= kPerThread) {
     const Eight v = *reinterpret_cast<const Eight*>(src);
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = v.w[i];
@@ -112,7 +113,7 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(MxQuantParams p
     for (int i = 0; i < kWords; ++i) w[i] = 0;
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i)
-      if (c0 + i < p.cols) w[i * kWords / 8] |= (uint32_t)src[i] << (kWords == 4 ? 16 * (i & 1) : 0);
+      if (i < left) w[i * kWords / 8] |= (uint32_t)src[i] << (kWords == 4 ? 16 * (i & 1) : 0);
   }
   uint32_t top = T::top(w);
   top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xF, 0xF, true));  // quad lanes 1 0 3 2
@@ -140,12 +141,12 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(MxQuantParams p
 #pragma unroll
       for (int i = 0; i < kWords; ++i) v.w[i] = T::kNan;
     }
-    if (c0 + kPerThread <= p.cols) {
+    if (left >= kPerThread) {
       *reinterpret_cast<Eight*>(dst) = v;
     } else {
 #pragma unroll
       for (int i = 0; i < kPerThread; ++i)
-        if (c0 + i < p.cols) dst[i] = (Elem)(v.w[i * kWords / 8] >> (kWords == 4 ? 16 * (i & 1) : 0));
+        if (i < left) dst[i] = (Elem)(v.w[i * kWords / 8] >> (kWords == 4 ? 16 * (i & 1) : 0));
     }
   }
 }
@@ -161,7 +162,7 @@ void launch_source(const MxQuantParams& p, dim3 grid, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_mx_quantize(const MxQuantParams& p, hipStream_t stream) {
-  const int64_t items = (int64_t)((p.cols + kMxBlock - 1) / kMxBlock) * (kMxBlock / kPerThread) * p.rows;
+  const int64_t items = ((int64_t)p.cols + kMxBlock - 1) / kMxBlock * (kMxBlock / kPerThread) * p.rows;
   const dim3 grid((unsigned)((items + kQuantThreads - 1) / kQuantThreads));
   if (p.source == kMxBf16) launch_source<Bf16>(p, grid, stream);
   else if (p.source == kMxF16) launch_source<F16>(p, grid, stream);
