@@ -162,3 +162,146 @@ def test_tensors_in_host_memory_are_refused(plan):
         with pytest.raises(q.QtipError) as ei:
             call()
         assert ei.value.status == ARG and ("GPU memory" in str(ei.value) or "device" in str(ei.value))
+
+
+@pytest.fixture
+def gpu_arrays(monkeypatch):
+    """torch, a maker of tensors that pass for arrays of GPU 0, and the list of calls that the binding lets through: none
+    reaches the library."""
+    torch = pytest.importorskip("torch")
+    binding = q._binding
+    real, calls = q.lib(), []
+
+    class Array(torch.Tensor):
+        place = 0
+
+        def get_device(self):
+            return self.place
+
+    class Library:
+        def __getattr__(self, name):
+            if name in ("qtip_status_string", "qtip_last_error_detail", "qtip_moe_plan_destroy"):
+                return getattr(real, name)
+            return lambda *args: calls.append((name, args)) or q.QTIP_OK
+
+    binding._find_torch()
+    monkeypatch.setattr(binding, "_get_device", lambda: 0)
+    monkeypatch.setattr(binding, "_stream", lambda stream: None)
+    monkeypatch.setattr(binding, "lib", lambda: Library())
+
+    def array(*shape, dtype="uint8", device=0):
+        t = torch.zeros(shape, dtype=getattr(torch, dtype)).as_subclass(Array)
+        t.place = device
+        return t
+    return torch, array, calls
+
+
+def refusals(call, good, bad, calls):
+    """`good` arguments go through; with each of `bad` in one's place the call is refused, naming it."""
+    call(**good)
+    assert len(calls) == 1
+    for name, value in bad:
+        args = dict(good, **{name: value()})
+        with pytest.raises(q.QtipError) as ei:
+            call(**args)
+        assert ei.value.status == ARG and name in str(ei.value), (name, str(ei.value))
+    assert len(calls) == 1
+
+
+def test_gate_route_takes_whole_arrays_of_its_types_only(gpu_arrays):
+    torch, array, calls = gpu_arrays
+    n, E, k = 5, 256, 6
+    plan = q._binding.Plan(0, q.make_desc(E, k, 4096, 2048, 64))
+    i32 = lambda *s: array(*s, dtype="int32")
+    f32 = lambda *s: array(*s, dtype="float32")
+    good = dict(bias=f32(E), logits=f32(n, E), topk_idx=i32(n, k), topk_w=f32(n, k), counts=i32(E), offsets=i32(E + 1),
+                sorted_pair=i32(n * k), tile_map=i32(n * k, 3), n_tiles=i32(1), workspace=array(512))
+    call = lambda bias, workspace, **a: q.qtip_moe_gate_route(
+        plan, q.make_gate(bias=bias), n_tokens=n, workspace=workspace, workspace_bytes=512, **a)
+    bad = [(name, lambda t=t: t.reshape(-1)[:-1].contiguous()) for name, t in good.items()]        # one short
+    bad += [(name, lambda t=t: t.half() if t.dtype == torch.float32 else t.long())                 # another type
+            for name, t in good.items() if name != "workspace"]
+    bad += [(name, lambda t=t: array(*t.shape, dtype=str(t.dtype)[6:], device=1)) for name, t in good.items()]
+    bad += [("logits", lambda: f32(E, n).t()), ("logits", lambda: torch.zeros(n, E)),
+            ("bias", lambda: f32(2 * E)[::2]), ("bias", lambda: torch.zeros(E)), ("topk_w", lambda: i32(n, k))]
+    refusals(call, good, bad, calls)
+
+
+def test_gated_layers_take_whole_arrays_of_their_types_only(gpu_arrays):
+    torch, array, calls = gpu_arrays
+    n, E, k, H, I = 5, 8, 2, 256, 128
+    for out_dtype, out_type in ((q.QTIP_OUT_F32, "float32"), (q.QTIP_OUT_BF16, "bfloat16")):
+        plan = q._binding.Plan(0, q.make_desc(E, k, H, I, 64, out_dtype=out_dtype))
+        good = dict(bias=array(E, dtype="float32"), x_bf16=array(n, H, dtype="bfloat16"),
+                    logits=array(n, E, dtype="float32"), out=array(n, H, dtype=out_type), workspace=array(512))
+        bad = [(name, lambda t=t: t.reshape(-1)[:-1].contiguous()) for name, t in good.items()]
+        bad += [("x_bf16", lambda: array(n, H, dtype="float16")), ("x_bf16", lambda: array(n, H, dtype="float32")),
+                ("logits", lambda: array(n, 2 * E, dtype="bfloat16")), ("bias", lambda: array(2 * E, dtype="bfloat16")),
+                ("out", lambda: array(n, H, dtype="float16")), ("out", lambda: array(n, H, dtype="float64")),
+                ("out", lambda: array(n, H, dtype=out_type, device=1))]
+        w = q.make_weights(*[256] * 7)
+        refusals(lambda bias, **a: q.qtip_moe_forward_gated(plan, w, q.make_gate(bias=bias), n_tokens=n,
+                                                            workspace_bytes=512, **a), good, bad, calls)
+        calls.clear()
+        names = ("codes_gate", "scales_gate", "codes_up", "scales_up", "codes_down", "scales_down")
+        good.update((name, array(E * H * I // (32 if "scales" in name else 2))) for name in names)
+        bad += [(name, lambda name=name: good[name][:-1].contiguous()) for name in names]
+        bad += [(name, lambda name=name: good[name].float()) for name in names]
+        bad += [("codes_up", lambda: array(E * H * I // 2, device=1)), ("scales_down", lambda: array(E * H * I)[::2]),
+                ("codes_down", lambda: torch.zeros(E * H * I // 2, dtype=torch.uint8))]
+        refusals(lambda bias, x_bf16, logits, out, workspace, **w: q.qtip_mx_moe_forward(
+            plan, q.make_mx_weights(**w), q.make_gate(bias=bias), x_bf16, logits, n, out, workspace, 512), good, bad, calls)
+        calls.clear()
+        q.qtip_mx_moe_forward(plan, q.make_mx_weights(*[256] * 6), None, good["x_bf16"].view(torch.int16), 256, n, 256,
+                              256, 512)          # addresses, and 16-bit patterns, as they come
+        assert len(calls) == 1
+        calls.clear()
+
+
+@pytest.mark.parametrize("part", [q.QTIP_MX_PASS_GATE_UP, q.QTIP_MX_PASS_DOWN])
+def test_expert_pass_takes_whole_arrays_of_its_types_only(gpu_arrays, part):
+    torch, array, calls = gpu_arrays
+    n, E, k, H, I = 5, 8, 2, 256, 128
+    plan = q._binding.Plan(0, q.make_desc(E, k, H, I, 64))
+    rows, cols, width = (n, H, I) if part == q.QTIP_MX_PASS_GATE_UP else (n * k, I, H)
+    good = dict(a_codes=array(rows, cols // 2), a_scales=array(rows, cols // 32), offsets=array(E + 1, dtype="int32"),
+                sorted_pair=array(n * k, dtype="int32"), out=array(n * k, width, dtype="bfloat16"))
+    own = ("gate", "up") if part == q.QTIP_MX_PASS_GATE_UP else ("down",)
+    weights = {f"{what}_{name}": array(E * H * I // (2 if what == "codes" else 32))
+               for name in own for what in ("codes", "scales")}
+    good.update(weights)
+    bad = [(name, lambda t=t: t.reshape(-1)[:-1].contiguous()) for name, t in good.items()]
+    bad += [(name, lambda t=t: array(*t.shape, dtype=str(t.dtype)[6:], device=1)) for name, t in good.items()]
+    bad += [("offsets", lambda: array(E + 1, dtype="int64")), ("sorted_pair", lambda: array(n * k, dtype="int64")),
+            ("a_codes", lambda: array(rows, cols, dtype="int32")), ("out", lambda: array(n * k, width, dtype="float32"))]
+
+    def call(a_codes, a_scales, offsets, sorted_pair, out, **w):
+        q.qtip_mx_expert_matmul(plan, part, q.make_mx_weights(**w), a_codes, a_scales, offsets, sorted_pair, n, out,
+                                q.QTIP_OUT_BF16)
+    refusals(call, good, bad, calls)
+    calls.clear()
+    call(**dict(good, **{name: array(1) for name in (f"{w}_{m}" for w in ("codes", "scales") for m in
+                                                     ("gate", "up", "down") if m not in own)}))   # not this pass's
+    assert len(calls) == 1
+
+
+def test_dense_mx_calls_take_arrays_of_their_types_only(gpu_arrays):
+    torch, array, calls = gpu_arrays
+    for kind, name, other in ((q.QTIP_MX_SRC_BF16, "bfloat16", "float16"), (q.QTIP_MX_SRC_F16, "float16", "bfloat16"),
+                              (q.QTIP_MX_SRC_F32, "float32", "int32")):
+        good = dict(src=array(4, 80, dtype=name)[:, :64], codes=array(4, 32), scales=array(4, 2),
+                    values=array(4, 64, dtype=name))
+        bad = [("src", lambda: array(4, 80, dtype=other)), ("src", lambda: array(4 * 80 - 17, dtype=name)),
+               ("src", lambda: array(4, 80, dtype=name, device=1)), ("values", lambda: array(4, 64, dtype=other)),
+               ("codes", lambda: array(4, 32, dtype="int32")), ("scales", lambda: array(7))]
+        refusals(lambda src, **a: q.qtip_mx_quantize(src, kind, 4, 64, 80, q.QTIP_MX_SCALE_FLOOR, **a), good, bad, calls)
+        calls.clear()
+    for kind, name, other in ((q.QTIP_OUT_BF16, "bfloat16", "float16"), (q.QTIP_OUT_F32, "float32", "int32")):
+        good = dict(a_codes=array(3, 32), a_scales=array(3, 2), w_codes=array(5, 32), w_scales=array(5, 2),
+                    out=array(3, 5, dtype=name))
+        bad = [(key, lambda t=t: t.reshape(-1)[:-1].contiguous()) for key, t in good.items()]
+        bad += [(key, lambda t=t: array(*t.shape, dtype=str(t.dtype)[6:], device=1)) for key, t in good.items()]
+        bad += [("out", lambda: array(3, 5, dtype=other)), ("w_scales", lambda: array(5, 2, dtype="float32"))]
+        refusals(lambda a_codes, a_scales, w_codes, w_scales, out: q.qtip_mx_matmul(
+            a_codes, a_scales, 3, w_codes, w_scales, 5, 64, out, kind), good, bad, calls)
+        calls.clear()

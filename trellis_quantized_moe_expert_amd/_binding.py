@@ -194,6 +194,9 @@ def _ptr(obj):
 _torch = None       # torch, once it has been needed; None again where it is not installed
 _get_device = None  # torch's current device and its stream's handle as plain calls: 0.4 us a call
 _get_stream = None  # against 3.6 through torch.cuda.current_stream()
+_types = {}         # by kind of array (_KINDS): the element types it may have, the usual one first
+_KINDS = {"f": "float32", "i": "int32", "b": "bfloat16 int16 uint16", "h": "float16 int16 uint16",
+          "u": "uint8 int8 float4_e2m1fn_x2 float8_e8m0fnu"}  # 16-bit values may come as their bits
 
 
 def _find_torch() -> bool:
@@ -206,6 +209,8 @@ def _find_torch() -> bool:
             return False
         _get_device = torch.cuda.current_device
         _get_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _types.update((kind, [getattr(torch, name) for name in names.split() if hasattr(torch, name)])
+                      for kind, names in _KINDS.items())
         _torch = torch
     return True
 
@@ -242,17 +247,26 @@ def make_weights(codes_gate, codes_up, codes_down, scale_gate, scale_up, scale_d
                                                 scale_down, lut)))
 
 
+class Plan(int):
+    """A plan's handle that knows its layer, for the checks of tensors' sizes: `layer` is (E, k, H, I, out_dtype)."""
+
+    def __new__(cls, handle: int, desc: qtip_moe_desc):
+        self = super().__new__(cls, handle)
+        self.layer = (desc.num_experts, desc.top_k, desc.hidden, desc.inter, desc.out_dtype)
+        return self
+
+
 # ---- the C entry points, same names --------------------------------------------------------
 def qtip_moe_plan(desc: qtip_moe_desc, device: int = 0) -> int:
     out = _P()
     _check("qtip_moe_plan", lib().qtip_moe_plan(ctypes.byref(desc), device, ctypes.byref(out)))
-    return out.value
+    return Plan(out.value, desc)
 
 
 def qtip_moe_plan_for_arch(desc: qtip_moe_desc, arch: str) -> int:
     out = _P()
     _check("qtip_moe_plan_for_arch", lib().qtip_moe_plan_for_arch(ctypes.byref(desc), arch.encode(), ctypes.byref(out)))
-    return out.value
+    return Plan(out.value, desc)
 
 
 def qtip_moe_plan_destroy(plan: int) -> None:
@@ -418,6 +432,7 @@ def make_gate(score=QTIP_GATE_SOFTMAX, num_groups=1, top_groups=1, group_top=1, 
     """A gate; it keeps the bias tensor alive."""
     g = qtip_moe_gate(score, num_groups, top_groups, group_top, renormalise, scale, _ptr(bias))
     g.keep = bias
+    g.seen = _seen("f", bias)
     return g
 
 
@@ -427,28 +442,103 @@ def make_mx_weights(codes_gate=None, scales_gate=None, codes_up=None, scales_up=
     arrays = (codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down)
     w = qtip_mx_weights(*(_ptr(a) for a in arrays))
     w.keep = arrays
+    w.seen = tuple(_seen("u", a) for a in arrays)
     return w
 
 
-def _on_device(fn: str, *items) -> None:
-    """Refuse tensors that are not whole arrays in the current GPU's memory: (name, object, bytes)s."""
+def _is_tensor(obj) -> bool:
+    return obj is not None and obj.__class__ is not int and _find_torch() and isinstance(obj, _torch.Tensor)
+
+
+def _fault(kind: str, obj) -> str:
+    """What is wrong with a tensor that stands for a whole array of a kind (".": any) in GPU memory."""
+    if obj.get_device() < 0:
+        return "is not in GPU memory"
+    if kind != "." and obj.dtype not in _types[kind]:
+        return f"has elements of {obj.dtype}, not of {_types[kind][0]}"
+    return "" if obj.is_contiguous() else "must be contiguous"
+
+
+def _refuse(fn: str, name: str, fault: str):
+    raise QtipError(fn, QTIP_ERR_INVALID_ARG, f"{name} {fault}")
+
+
+def _refuse_place(fn: str, name: str, device: int, have: int, size: int) -> None:
+    if device != _get_device():
+        _refuse(fn, name, f"is not on the current device (cuda:{_get_device()})")
+    if have < size:
+        _refuse(fn, name, f"is smaller than {size} bytes")
+
+
+def _seen(kind: str, obj):
+    """(fault, device, bytes) of a tensor whose address a struct takes; None of anything else."""
+    return (_fault(kind, obj), obj.get_device(), obj.nbytes) if _is_tensor(obj) else None
+
+
+def _check_seen(fn: str, name: str, facts: tuple, size: int) -> None:
+    if facts[0]:
+        _refuse(fn, name, facts[0])
+    if facts[1] != _get_device() or facts[2] < size:
+        _refuse_place(fn, name, facts[1], facts[2], size)
+
+
+def _pointers(fn: str, kinds: str, names: tuple, objs: tuple, sizes: tuple) -> list:
+    """The addresses of a call's arrays.  Tensors have to be whole arrays of their kind (a letter of _KINDS each, "."
+    for any) and of at least so many bytes in the current GPU's memory; other objects are taken as they come."""
     if _torch is None and not _find_torch():
-        return
-    dev = None
-    for name, obj, size in items:
-        if obj is None or obj.__class__ is int or not isinstance(obj, _torch.Tensor):
-            continue
-        where = obj.get_device()
-        if where < 0:
-            raise QtipError(fn, QTIP_ERR_INVALID_ARG, f"{name} is not in GPU memory")
-        if dev is None:
-            dev = _get_device()
-        if where != dev:
-            raise QtipError(fn, QTIP_ERR_INVALID_ARG, f"{name} is not on the current device (cuda:{dev})")
-        if obj.nbytes < size:
-            raise QtipError(fn, QTIP_ERR_INVALID_ARG, f"{name} is smaller than {size} bytes")
-        if not obj.is_contiguous():
-            raise QtipError(fn, QTIP_ERR_INVALID_ARG, f"{name} must be contiguous")
+        return [_ptr(o) for o in objs]
+    usual = _types.get(kinds)
+    if usual is None:
+        usual = _types[kinds] = [_types["u" if kind == "." else kind][0] for kind in kinds]
+    tensor, device, out = _torch.Tensor, None, []
+    for obj, dtype, size in zip(objs, usual, sizes):
+        if obj.__class__ is tensor:
+            where = obj.get_device()
+            if device is None and where >= 0:
+                device = _get_device()
+            if where == device and obj.dtype is dtype and obj.nbytes >= size and obj.is_contiguous():
+                out.append(obj.data_ptr())
+                continue
+        i = len(out)
+        if isinstance(obj, tensor):
+            fault = _fault(kinds[i], obj)
+            if fault:
+                _refuse(fn, names[i], fault)
+            _refuse_place(fn, names[i], obj.get_device(), obj.nbytes, size)
+        out.append(_ptr(obj))
+    return out
+
+
+def _layer(plan) -> tuple:
+    """(E, k, H, I, out_dtype) of a plan; None of a handle that was not made here, whose arrays' sizes go unchecked."""
+    return getattr(plan, "layer", None)
+
+
+def _check_mx_weights(fn: str, weights, layer, first: int, last: int) -> None:
+    """Arrays [first, last) of the struct's six: a matrix has H I values, two codes a byte, 32 to a scale."""
+    codes = layer[0] * layer[2] * layer[3] // 2 if layer else 0
+    device = None
+    for facts in getattr(weights, "seen", ())[first:last]:
+        if facts is not None:
+            device = _get_device() if device is None and not facts[0] else device
+            size = codes if first & 1 == 0 else codes // 16
+            if facts[0] or facts[1] != device or facts[2] < size:
+                _check_seen(fn, qtip_mx_weights._fields_[first][0], facts, size)
+        first += 1
+
+
+def _check_bias(fn: str, gate, layer) -> None:
+    facts = getattr(gate, "seen", None)
+    if facts is not None:
+        _check_seen(fn, "bias", facts, 4 * layer[0] if layer else 0)
+
+
+def _out_kind(out_dtype: int) -> tuple:
+    return ("f", 4) if out_dtype == QTIP_OUT_F32 else ("b", 2)
+
+
+_ROUTE_NAMES = ("logits", "topk_idx", "topk_w", "counts", "offsets", "sorted_pair", "workspace", "tile_map", "n_tiles")
+_SRC_KINDS = {QTIP_MX_SRC_BF16: ("b", 2), QTIP_MX_SRC_F16: ("h", 2), QTIP_MX_SRC_F32: ("f", 4)}
 
 
 def qtip_moe_gate_workspace_bytes(plan) -> int:
@@ -457,57 +547,83 @@ def qtip_moe_gate_workspace_bytes(plan) -> int:
 
 def qtip_moe_gate_route(plan, gate: qtip_moe_gate, logits, n_tokens, topk_idx, topk_w, counts, offsets, sorted_pair,
                         tile_map, n_tiles, workspace, workspace_bytes, stream=None) -> None:
-    _on_device("qtip_moe_gate_route", ("logits", logits, 0), ("topk_idx", topk_idx, 0), ("topk_w", topk_w, 0),
-               ("counts", counts, 0), ("offsets", offsets, 0), ("sorted_pair", sorted_pair, 0),
-               ("tile_map", tile_map, 0), ("n_tiles", n_tiles, 4), ("workspace", workspace, workspace_bytes),
-               ("bias", getattr(gate, "keep", None), 0))
-    _check("qtip_moe_gate_route", lib().qtip_moe_gate_route(
-        plan, ctypes.byref(gate), _ptr(logits), n_tokens, _ptr(topk_idx), _ptr(topk_w), _ptr(counts), _ptr(offsets),
-        _ptr(sorted_pair), _ptr(tile_map), _ptr(n_tiles), _ptr(workspace), workspace_bytes, _stream(stream)))
+    fn, layer = "qtip_moe_gate_route", _layer(plan)
+    E, k = layer[:2] if layer else (-1, 0)
+    pairs = 4 * n_tokens * k
+    objs = logits, topk_idx, topk_w, counts, offsets, sorted_pair, workspace
+    sizes = 4 * n_tokens * E, pairs, pairs, 4 * E, 4 * E + 4, pairs, workspace_bytes
+    if tile_map is None and n_tiles is None:
+        p = _pointers(fn, "fifiii.", _ROUTE_NAMES, objs, sizes)
+        p += [None, None]
+    else:
+        p = _pointers(fn, "fifiii.ii", _ROUTE_NAMES, (*objs, tile_map, n_tiles), (*sizes, 3 * pairs, 4))
+    _check_bias(fn, gate, layer)
+    _check(fn, lib().qtip_moe_gate_route(plan, ctypes.byref(gate), p[0], n_tokens, p[1], p[2], p[3], p[4], p[5], p[7],
+                                         p[8], p[6], workspace_bytes, _stream(stream)))
+
+
+def _layer_pointers(fn: str, layer, x_bf16, logits, n_tokens: int, out, workspace, workspace_bytes: int) -> list:
+    E, _, H, _, out_dtype = layer or (0, 0, 0, 0, None)
+    kind, size = (".", 0) if out_dtype is None else _out_kind(out_dtype)
+    return _pointers(fn, "bf" + kind + ".", ("x_bf16", "logits", "out", "workspace"), (x_bf16, logits, out, workspace),
+                     (2 * n_tokens * H, 4 * n_tokens * E, size * n_tokens * H, workspace_bytes))
 
 
 def qtip_moe_forward_gated(plan, weights: qtip_moe_weights, gate: qtip_moe_gate, x_bf16, logits, n_tokens, out,
                            workspace, workspace_bytes, stream=None) -> None:
-    _on_device("qtip_moe_forward_gated", ("x_bf16", x_bf16, 0), ("logits", logits, 0), ("out", out, 0),
-               ("workspace", workspace, workspace_bytes), ("bias", getattr(gate, "keep", None), 0))
-    _check("qtip_moe_forward_gated", lib().qtip_moe_forward_gated(
-        plan, ctypes.byref(weights), ctypes.byref(gate), _ptr(x_bf16), _ptr(logits), n_tokens, _ptr(out),
-        _ptr(workspace), workspace_bytes, _stream(stream)))
+    fn, layer = "qtip_moe_forward_gated", _layer(plan)
+    p = _layer_pointers(fn, layer, x_bf16, logits, n_tokens, out, workspace, workspace_bytes)
+    _check_bias(fn, gate, layer)
+    _check(fn, lib().qtip_moe_forward_gated(plan, ctypes.byref(weights), ctypes.byref(gate), p[0], p[1], n_tokens, p[2],
+                                            p[3], workspace_bytes, _stream(stream)))
 
 
 def qtip_mx_quantize(src, src_type, rows, cols, row_stride, scale_rule, codes, scales, values=None,
                      stream=None) -> None:
+    fn = "qtip_mx_quantize"
     blocks = (cols + QTIP_MX_BLOCK - 1) // QTIP_MX_BLOCK
-    size = 4 if src_type == QTIP_MX_SRC_F32 else 2
+    kind, size = _SRC_KINDS.get(src_type, (".", 0))
     if (_torch is not None or _find_torch()) and isinstance(src, _torch.Tensor):  # rows of a wider tensor are welcome
         if src.get_device() < 0 or src.get_device() != _get_device():
-            raise QtipError("qtip_mx_quantize", QTIP_ERR_INVALID_ARG, "src is not on the current device")
-        if src.element_size() != size:
-            raise QtipError("qtip_mx_quantize", QTIP_ERR_INVALID_ARG, f"src has no elements of {size} bytes")
-        if src.numel() == 0 or sum((n - 1) * st for n, st in zip(src.shape, src.stride())) < (
-                (rows - 1) * row_stride + cols - 1):
-            raise QtipError("qtip_mx_quantize", QTIP_ERR_INVALID_ARG, "src is smaller than its rows")
-    _on_device("qtip_mx_quantize", ("codes", codes, rows * blocks * 16), ("scales", scales, rows * blocks),
-               ("values", values, rows * cols * size))
-    _check("qtip_mx_quantize", lib().qtip_mx_quantize(_ptr(src), src_type, rows, cols, row_stride, scale_rule,
-                                                      _ptr(codes), _ptr(scales), _ptr(values), _stream(stream)))
+            _refuse(fn, "src", "is not on the current device")
+        if kind != "." and src.dtype not in _types[kind]:
+            _refuse(fn, "src", f"has elements of {src.dtype}, not of {_types[kind][0]}")
+        last = (rows - 1) * row_stride + cols
+        if src.numel() < last or not src.is_contiguous():
+            if src.numel() == 0 or sum((n - 1) * st for n, st in zip(src.shape, src.stride())) < last - 1:
+                _refuse(fn, "src", "is smaller than its rows")
+    sizes = 16 * rows * blocks, rows * blocks, rows * cols * size
+    if values is None:
+        p = _pointers(fn, "uu", ("codes", "scales"), (codes, scales), sizes)
+        p.append(None)
+    else:
+        p = _pointers(fn, "uu" + kind, ("codes", "scales", "values"), (codes, scales, values), sizes)
+    _check(fn, lib().qtip_mx_quantize(_ptr(src), src_type, rows, cols, row_stride, scale_rule, p[0], p[1], p[2],
+                                      _stream(stream)))
 
 
 def qtip_mx_matmul(a_codes, a_scales, m, w_codes, w_scales, n, k, out, out_dtype, stream=None) -> None:
-    _on_device("qtip_mx_matmul", ("a_codes", a_codes, m * k // 2), ("a_scales", a_scales, m * k // 32),
-               ("w_codes", w_codes, n * k // 2), ("w_scales", w_scales, n * k // 32),
-               ("out", out, m * n * (4 if out_dtype == QTIP_OUT_F32 else 2)))
-    _check("qtip_mx_matmul", lib().qtip_mx_matmul(_ptr(a_codes), _ptr(a_scales), m, _ptr(w_codes), _ptr(w_scales), n,
-                                                  k, _ptr(out), out_dtype, _stream(stream)))
+    kind, size = _out_kind(out_dtype)
+    p = _pointers("qtip_mx_matmul", "uuuu" + kind, ("a_codes", "a_scales", "w_codes", "w_scales", "out"),
+                  (a_codes, a_scales, w_codes, w_scales, out),
+                  (m * k // 2, m * k // 32, n * k // 2, n * k // 32, m * n * size))
+    _check("qtip_mx_matmul", lib().qtip_mx_matmul(p[0], p[1], m, p[2], p[3], n, k, p[4], out_dtype, _stream(stream)))
 
 
 def qtip_mx_expert_matmul(plan, pass_, weights: qtip_mx_weights, a_codes, a_scales, offsets, sorted_pair, n_tokens,
                           out, out_dtype, stream=None) -> None:
-    _on_device("qtip_mx_expert_matmul", ("a_codes", a_codes, 0), ("a_scales", a_scales, 0), ("offsets", offsets, 0),
-               ("sorted_pair", sorted_pair, 0), ("out", out, 0))
-    _check("qtip_mx_expert_matmul", lib().qtip_mx_expert_matmul(
-        plan, pass_, ctypes.byref(weights), _ptr(a_codes), _ptr(a_scales), _ptr(offsets), _ptr(sorted_pair), n_tokens,
-        _ptr(out), out_dtype, _stream(stream)))
+    fn, layer = "qtip_mx_expert_matmul", _layer(plan)
+    E, k, H, I, _ = layer or (-1, 0, 0, 0, None)
+    pairs = n_tokens * k
+    gate_up = pass_ == QTIP_MX_PASS_GATE_UP
+    values, width = (n_tokens * H, I) if gate_up else (pairs * I, H)
+    kind, size = _out_kind(out_dtype)
+    p = _pointers(fn, "uuii" + kind, ("a_codes", "a_scales", "offsets", "sorted_pair", "out"),
+                  (a_codes, a_scales, offsets, sorted_pair, out),
+                  (values // 2, values // 32, 4 * E + 4, 4 * pairs, pairs * width * size))
+    _check_mx_weights(fn, weights, layer, 0 if gate_up else 4, 4 if gate_up else 6)
+    _check(fn, lib().qtip_mx_expert_matmul(plan, pass_, ctypes.byref(weights), p[0], p[1], p[2], p[3], n_tokens, p[4],
+                                           out_dtype, _stream(stream)))
 
 
 def qtip_mx_moe_workspace_bytes(plan) -> int:
@@ -516,11 +632,12 @@ def qtip_mx_moe_workspace_bytes(plan) -> int:
 
 def qtip_mx_moe_forward(plan, weights: qtip_mx_weights, gate, x_bf16, logits, n_tokens, out, workspace,
                         workspace_bytes, stream=None) -> None:
-    _on_device("qtip_mx_moe_forward", ("x_bf16", x_bf16, 0), ("logits", logits, 0), ("out", out, 0),
-               ("workspace", workspace, workspace_bytes), ("bias", getattr(gate, "keep", None), 0))
-    _check("qtip_mx_moe_forward", lib().qtip_mx_moe_forward(
-        plan, ctypes.byref(weights), None if gate is None else ctypes.byref(gate), _ptr(x_bf16), _ptr(logits),
-        n_tokens, _ptr(out), _ptr(workspace), workspace_bytes, _stream(stream)))
+    fn, layer = "qtip_mx_moe_forward", _layer(plan)
+    p = _layer_pointers(fn, layer, x_bf16, logits, n_tokens, out, workspace, workspace_bytes)
+    _check_bias(fn, gate, layer)
+    _check_mx_weights(fn, weights, layer, 0, 6)
+    _check(fn, lib().qtip_mx_moe_forward(plan, ctypes.byref(weights), None if gate is None else ctypes.byref(gate),
+                                         p[0], p[1], n_tokens, p[2], p[3], workspace_bytes, _stream(stream)))
 
 
 def raw_status(fn_name: str, *args) -> int:
