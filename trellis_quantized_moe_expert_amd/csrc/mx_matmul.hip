@@ -664,24 +664,28 @@ template <int HALVES>
 hipError_t launch_halves(const MxMatmulParams& p, hipStream_t stream, bool launch) {
   // the tiled kernel reads 16 scales at a time and addresses a tile's rows by 31-bit offsets
   const bool tiles = (int64_t)p.a_rows * p.blocks >= 16 && (int64_t)p.E * p.n * p.blocks >= 16 && p.blocks < 1 << 18;
-  const int64_t row_blocks = ((int64_t)p.n + 15) / 16;
-  const bool few = p.offsets ? p.m <= 8 || (p.m <= 16 && p.m * row_blocks <= 1280) : p.m <= 16;
-  if (few && !p.offsets && p.blocks >= 128) return launch_direct<1, HALVES, 8>(p, stream, launch);
-  if (few) return launch_direct<1, HALVES, 4>(p, stream, launch);
-  if (!tiles || (!p.offsets && p.m <= 64 && p.n <= 4096)) return launch_direct<2, HALVES, 4>(p, stream, launch);
   if (p.offsets) {
+    const int64_t row_blocks = ((int64_t)p.n + 15) / 16;
+    if (p.m <= 8 || (p.m <= 16 && p.m * row_blocks <= 1280)) return launch_direct<1, HALVES, 4>(p, stream, launch);
+    if (!tiles) return launch_direct<2, HALVES, 4>(p, stream, launch);
     const int fill = (p.m + p.E - 1) / p.E;  // pairs an expert gets on average
     if (fill <= 28) return launch_tiled<32, 128, 1, 4, 2, 2, HALVES>(p, stream, launch);
     if (fill <= 160) return launch_tiled<128, 128, 2, 2, 4, 1, HALVES>(p, stream, launch);
     return launch_tiled<256, 256, 2, 4, 4, 1, HALVES>(p, stream, launch);
   }
-  auto groups = [&](int64_t bm, int64_t bn) { return (p.m + bm - 1) / bm * ((p.n + bn - 1) / bn); };
-  if (groups(256, 256) >= 256) return launch_tiled<256, 256, 2, 4, 4, 1, HALVES>(p, stream, launch);
-  if (groups(128, 128) >= 200) return launch_tiled<128, 128, 2, 2, 2, 2, HALVES>(p, stream, launch);
-  if (groups(64, 128) >= 256) return launch_tiled<64, 128, 1, 4, 2, 2, HALVES>(p, stream, launch);
-  if (groups(32, 128) > 256) return launch_tiled<32, 128, 1, 4, 2, 2, HALVES>(p, stream, launch);
-  if (groups(32, 128) >= 128) return launch_tiled<32, 128, 1, 4, 4, 2, HALVES>(p, stream, launch);
-  return launch_tiled<32, 64, 1, 2, 4, 2, HALVES>(p, stream, launch);
+  if constexpr (HALVES == 1) {  // a dense product is of one matrix
+    if (p.m <= 16 && p.blocks >= 128) return launch_direct<1, 1, 8>(p, stream, launch);
+    if (p.m <= 16) return launch_direct<1, 1, 4>(p, stream, launch);
+    if (!tiles || (p.m <= 64 && p.n <= 4096)) return launch_direct<2, 1, 4>(p, stream, launch);
+    auto groups = [&](int64_t bm, int64_t bn) { return (p.m + bm - 1) / bm * ((p.n + bn - 1) / bn); };
+    if (groups(256, 256) >= 256) return launch_tiled<256, 256, 2, 4, 4, 1, 1>(p, stream, launch);
+    if (groups(128, 128) >= 200) return launch_tiled<128, 128, 2, 2, 2, 2, 1>(p, stream, launch);
+    if (groups(64, 128) >= 256) return launch_tiled<64, 128, 1, 4, 2, 2, 1>(p, stream, launch);
+    if (groups(32, 128) > 256) return launch_tiled<32, 128, 1, 4, 2, 2, 1>(p, stream, launch);
+    if (groups(32, 128) >= 128) return launch_tiled<32, 128, 1, 4, 4, 2, 1>(p, stream, launch);
+    return launch_tiled<32, 64, 1, 2, 4, 2, 1>(p, stream, launch);
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
