@@ -189,3 +189,78 @@ def test_mx_layer_captured_and_beside_another():
         assert torch.equal(out_b, first_b)
     a.close()
     b.close()
+
+
+def gated_layer(shape, seed, arm, logits, bias, gate):
+    """A trellis layer behind a gate: (GPU output, the oracle's, the oracle's expert ids)."""
+    import torch
+    inp = moe_inputs.make_inputs(shape, seed=seed)
+    n, E, k, H = shape.n_tokens, shape.num_experts, shape.top_k, shape.hidden
+    inp.logits[:] = logits
+    layer = Layer(inp, arm=arm)
+    t = tokens_to_device(inp)
+    out = torch.full((n, H), float("nan"), dtype=torch.float32, device="cuda:0")
+    layer.ws.fill_(255)                   # NaN wherever a left-out pair's row would be read
+    q.qtip_moe_forward_gated(layer.plan, layer.w, make_gate(torch.from_numpy(bias).cuda(), **gate), t.x, t.logits, n, out,
+                             layer.ws, layer.ws.numel())
+    torch.cuda.synchronize()
+    got = out.cpu().numpy()
+    layer.close()
+    idx, w = oracle.route(inp.logits, bias, k, **gate)
+    _, offsets, order = oracle.bins(idx, E)
+    y = {p: np.zeros(H) for p in range(n * k)}
+    for e in np.unique(idx[idx >= 0]):
+        pids = order[offsets[e]:offsets[e + 1]]
+        y.update(zip(pids.tolist(), moe.expert_pairs(inp, e, pids)[0]))
+    return got, moe.combine(y, w, range(n), k, H), idx
+
+
+@pytest.mark.parametrize("rung", ["bitshift", "lut"])
+@pytest.mark.parametrize("n,E,k,gate", [
+    (1, 8, 3, GATE), (1, 300, 6, dict(GATE, group_top=1)), (1, 320, 10, dict(GATE, num_groups=32, top_groups=5)),
+    (2, 130, 9, dict(renormalise=0)), (24, 260, 4, GATE), (40, 96, 12, dict(score="sigmoid"))])
+def test_gated_trellis_layer_of_one_token_and_of_many_experts(n, E, k, gate, rung):
+    rng = np.random.default_rng(E + k)
+    say(f"gated trellis layer n={n} E={E} k={k} {rung}")
+    shape = moe_inputs.MoEShape(E, k, 256, 128, n, rung=rung)
+    logits = rng.standard_normal((n, E)).astype(np.float32)
+    if n == 24:
+        logits[5, 3:] = -np.inf           # fewer experts left than choices
+    got, want, idx = gated_layer(shape, 6, q.QTIP_ARM_AUTO, logits, (0.1 * rng.standard_normal(E)).astype(np.float32),
+                                 dict(dict(score="softmax"), **gate))
+    ok, st = parity.check_f32(got, want)
+    assert ok, st
+    assert (idx >= 0).any() and np.abs(got).max() > 0
+
+
+@pytest.mark.parametrize("rung", ["bitshift", "lut"])
+@pytest.mark.parametrize("n,arm", [(1, q.QTIP_ARM_AUTO), (1, q.QTIP_ARM_GROUPED), (20, q.QTIP_ARM_GEMV),
+                                   (20, q.QTIP_ARM_GROUPED), (20, q.QTIP_ARM_DEQUANT), (200, q.QTIP_ARM_GROUPED)])
+def test_gated_trellis_layer_without_any_expert(n, arm, rung):
+    say(f"gated trellis layer n={n} arm={arm} {rung}, no expert left")
+    shape = moe_inputs.MoEShape(8, 3, 256, 128, n, rung=rung)
+    logits = np.full((n, 8), -np.inf, np.float32)
+    got, _, idx = gated_layer(shape, 7, arm, logits, np.zeros(8, np.float32), GATE)
+    assert np.all(idx == -1) and np.all(got == 0)
+
+
+def test_mx_layer_without_any_expert_and_of_many():
+    import torch
+    say("mx layer, no expert left; 300 experts, 10 choices")
+    rng = np.random.default_rng(9)
+    for n in (1, 40):
+        layer = MxLayer(3, n, 8, 2, 256, 128, "fp32")
+        x, _ = tokens(rng, n, 256, 8)
+        out = layer.out()
+        layer.forward(make_gate(None, **GATE), x, torch.full((n, 8), -float("inf"), device="cuda:0"), out)
+        torch.cuda.synchronize()
+        assert bool((out == 0).all())
+        layer.close()
+        layer = MxLayer(4, n, 300, 10, 128, 128, "fp32")
+        x, logits = tokens(rng, n, 128, 300)
+        gate, lg, out = make_gate(None, "sigmoid", num_groups=4, top_groups=2), torch.from_numpy(logits).cuda(), layer.out()
+        layer.forward(gate, x, lg, out)
+        torch.cuda.synchronize()
+        ref, lim, idx = layer.steps(gate, x, lg)
+        assert np.all(idx >= 0) and np.all(np.abs(out.double().cpu().numpy() - ref) <= lim)
+        layer.close()
