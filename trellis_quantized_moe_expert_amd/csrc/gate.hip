@@ -24,9 +24,9 @@
 // on the fp64 values.
 //
 // What bounds it: the issue of fp64 instructions, not memory.  16384 tokens of 256 experts, 8 choices
-// from the best 4 of 8 groups, sigmoid with bias (16.8 MB of logits, 3.9 us at the copy rate) take 21 us
-// in the gate and 9 in placing, where each of 256 workgroups adds up all blocks' counts out of L2; 28 for
-// the call.  A wave of four tokens issues 1860 vector instructions, about 700 of them fp64 (half for the
+// from the best 4 of 8 groups, sigmoid with bias (16.8 MB of logits, 3.9 us at the copy rate) take 21.7 us
+// in the gate and 9 in placing, where each of 256 workgroups adds up all blocks' counts out of L2; 28 to 29 for
+// the call.  A wave of four tokens issues 1870 vector instructions, about 700 of them fp64 (half for the
 // 16 sigmoids of a lane, half for the sort and the merges).  With the constants
 // and lane masks of a loop over tokens kept in vector registers the kernel spilled and took 25.  Small
 // batches are bound by launches and the latency of a chain of dependent steps: a token of 8 choices,

@@ -36,7 +36,7 @@ __device__ inline uint32_t bf16_pair(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)lo, (__bf16)hi});
 }
 
-// silu(g) u.  exp(-g) = inf makes the reciprocal 0 and the result -0, the limit.
+// silu(g) u.  From exp(-g) = 2^126 on the reciprocal is 0 and the result -0: silu itself is under 2^-119 there.
 __device__ inline float swiglu(float g, float u) { return g * __builtin_amdgcn_rcpf(1.0f + expf(-g)) * u; }
 
 // The t-th tile of at most bm pairs of one expert, experts ascending: its expert, first place in
@@ -659,6 +659,9 @@ hipError_t launch_tiled(const MxMatmulParams& p, hipStream_t stream, bool launch
 //     of 32 x 128        128 x 2048 x 4096 (64) 7.7, 8.2; 128 x 8192 x 2048 (256) 7.3, 6.7
 //   experts              6 pairs direct 13.5, 32 x 128 15.8; 12 pairs 21.2, 20.0; 24 pairs an expert 32 x 128 458,
 //                        128 x 128 485; 48 pairs 588, 533; 96 pairs 128 x 128 565, 256 x 256 659; 192 pairs 1050, 752
+// The experts' points are of uniform routing, where every tile makes thousands of workgroups.  Of few or small
+// experts the large tiles make fewer than there are CUs, and under skewed routing the average says little
+// about a woken expert's pairs: neither is measured, and the rule does not ask.
 // Without `launch` it says whether the launch could be made.
 template <int HALVES>
 hipError_t launch_halves(const MxMatmulParams& p, hipStream_t stream, bool launch) {
