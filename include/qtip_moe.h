@@ -440,8 +440,9 @@ qtip_status qtip_moe_gate_route(qtip_moe_plan_t plan, const qtip_moe_gate* gate 
                                 void* workspace, size_t workspace_bytes, void* stream);
 
 /* The layer of qtip_moe_forward with its experts and weights chosen by a gate.  A token's left-out
- * slots add nothing to its output; a token without any expert gets zeros.  Workspace and errors as
- * qtip_moe_forward; a bad gate -> INVALID_ARG. */
+ * slots add nothing to its output; a token without any expert gets zeros.  Small batches too are routed
+ * and combined in launches of their own, whatever qtip_moe_plan_schedule says of qtip_moe_forward.
+ * Workspace and errors as qtip_moe_forward; a bad gate -> INVALID_ARG. */
 qtip_status qtip_moe_forward_gated(qtip_moe_plan_t plan, const qtip_moe_weights* w /*host struct of device ptrs*/,
                                    const qtip_moe_gate* gate /*host struct*/, const void* x_bf16, const float* logits,
                                    int32_t n_tokens, void* out, void* workspace, size_t workspace_bytes,
