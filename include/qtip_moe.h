@@ -6,7 +6,8 @@
  * expert into m-tiles; every woken expert's packed bytes are decoded inside the
  * multiply, so dense weights never exist in memory.  The layer can also route through a gate
  * (scores, a balance bias, groups), and its experts can be MXFP4 matrices (4-bit microscaled
- * values) on the scaled matrix instructions instead of trellis codes.
+ * values) on the scaled matrix instructions instead of trellis codes, or e4m3 matrices (8-bit
+ * floating point with a scale for each 128 x 128 block), with the norm in front of the layer.
  *
  * Sources (the pages this library implements):
  *  - m-tile occupancy page, PR #167 "gate the trellis grouped GEMM on m-tile
@@ -83,7 +84,7 @@ typedef enum qtip_status {
  * shared by up to 64 binned pairs, MFMA), and the dequantize arm (the woken experts' weights
  * materialised as dense bf16 in the workspace, then an MFMA pass over them). */
 enum { QTIP_ARM_AUTO = 0, QTIP_ARM_GEMV = 1, QTIP_ARM_GROUPED = 2, QTIP_ARM_DEQUANT = 3 };
-enum { QTIP_OUT_BF16 = 0, QTIP_OUT_F32 = 1 };
+enum { QTIP_OUT_BF16 = 0, QTIP_OUT_F32 = 1, QTIP_OUT_E4M3 = 2 /* the fused e4m3 expert pass only */ };
 enum { QTIP_ACT_AUTO = 0, QTIP_ACT_ROWS = 1, QTIP_ACT_FRAGMENTS = 2 };
 /* The two 2-bit rungs (weight formats) of the expert matrices; see "Weight formats" above. */
 enum { QTIP_RUNG_BITSHIFT = 0, QTIP_RUNG_LUT = 1 };
@@ -527,6 +528,103 @@ qtip_status qtip_mx_moe_forward(qtip_moe_plan_t plan, const qtip_mx_weights* w /
                                 const qtip_moe_gate* gate /*host struct or NULL*/, const void* x_bf16,
                                 const float* logits, int32_t n_tokens, void* out, void* workspace,
                                 size_t workspace_bytes, void* stream);
+
+/* ---- e4m3: 8-bit floating point with a scale for each block of 128 --------------------------
+ * Values are e4m3 codes (four bits of exponent, three of mantissa, no infinities, 0x7f and 0xff NaN; the
+ * largest is 448) times an fp32 scale.  Activations have a scale for each 128 values of a row (the row's last
+ * block may be shorter), weight matrices one for each 128 x 128 block (the last ones may be smaller).  Codes
+ * are row-major, a row of `cols` values taking cols rounded up to 16 bytes (zeros behind its end); scales are
+ * row-major [rows][ceil(cols / 128)] or [ceil(rows / 128)][ceil(cols / 128)]: the layout of the checkpoints that
+ * hold such weights.
+ *   QTIP_F8_SCALE_AMAX  scale = amax / 448 rounded to fp32, amax the block's largest magnitude
+ *   QTIP_F8_SCALE_POW2  scale = the smallest power of two that is no less than amax / 448
+ *   Both are at least 2^-126 (a block of zeros has that).  A code is the e4m3 value nearest to x / scale (of the
+ *   scale as stored, as if divided exactly), a tie the even code; the sign is x's.  A block with a NaN or an
+ *   infinity gets the scale NaN and zero codes: it stands for NaNs.
+ *
+ * qtip_f8_quantize: rows of bf16, fp16 or fp32 values to codes and scales.  block_rows 1 (activations) or 128
+ *   (weights).  src [rows] rows of cols elements, row_stride >= cols elements apart, aligned to its type;
+ *   codes 16-byte, scales 4-byte aligned; no output may overlap src.  rows and cols >= 1 (else INVALID_CONFIG);
+ *   rows x ceil(cols / 128) at most 2^28 - 16 (block_rows 128: at most 2^24 - 1 blocks), row_stride below
+ *   2^40.  Errors: NULL, a bad type, rule or block_rows, row_stride < cols, misalignment, sizes past the limits
+ *   -> INVALID_ARG; else as qtip_moe_route. */
+enum { QTIP_F8_BF16 = 0, QTIP_F8_F16 = 1, QTIP_F8_F32 = 2 };
+enum { QTIP_F8_SCALE_AMAX = 0, QTIP_F8_SCALE_POW2 = 1 };
+#define QTIP_F8_BLOCK 128
+qtip_status qtip_f8_quantize(const void* src, int32_t src_type, int32_t rows, int32_t cols, int64_t row_stride,
+                             int32_t block_rows, int32_t scale_rule, uint8_t* codes, float* scales, void* stream);
+
+/* RMS norm with the residual's addition and an e4m3 output, the step in front of a layer:
+ *   h = x, or where residual is not NULL x + residual rounded to `type` and written to residual_out
+ *   y_c = h_c w_c / sqrt(sum_i h_i^2 / cols + eps)                   in fp32
+ *   codes and scales (a scale for each 128 of a row) of y; where values is not NULL y rounded to `type` too
+ * x [rows] rows of cols elements of `type` (QTIP_F8_BF16, _F16 or _F32), x_stride apart; residual and residual_out
+ * likewise, residual_stride apart (not read without a residual); residual_out may be residual itself (in place),
+ * and must be NULL without one; weight [cols] of weight_type (any of the three); values [rows][cols] of
+ * `type`.  Outputs may not overlap inputs or each other but for that.  x, residual, residual_out and weight
+ * aligned to their type, codes and values 16-byte, scales 4-byte aligned.  eps finite and >= 0 (a row of zeros with
+ * eps 0 is NaN, as the formula says).  The sum of squares is fp32, and fp64 where the row's squares leave fp32's range.
+ * A NaN in a row makes its whole y NaN, an infinity its own block (the others become zeros).
+ * rows and cols >= 1 (else INVALID_CONFIG); rows below 2^22, cols at most 2^30, strides below 2^40.
+ * Errors: NULL x, weight, codes or scales, one of residual and residual_out NULL without the other, a bad
+ * type, rule or eps, a stride < cols, misalignment, sizes past the limits -> INVALID_ARG; else as qtip_moe_route. */
+qtip_status qtip_f8_rms_norm(const void* x, int32_t type, int32_t rows, int32_t cols, int64_t x_stride,
+                             const void* residual, int64_t residual_stride, void* residual_out, const void* weight,
+                             int32_t weight_type, float eps, int32_t scale_rule, uint8_t* codes, float* scales,
+                             void* values, void* stream);
+
+/* out[i][r] = sum_b a_scales[i][b] w_scales[r / 128][b] sum_{c in b} a[i][c] w[r][c], i < m, r < n, over the blocks b
+ * of 128 of k inputs: both operands e4m3, products exact and sums in fp32 on v_mfma_f32_16x16x32_bf16, out [m][n]
+ * bf16 or fp32 (out_dtype).  k must be a multiple of 16 (a row that qtip_f8_quantize filled up has k = its bytes); the
+ * last block may be shorter than 128, and so may the last rows of w.  The product of a block's two scales has to
+ * be an fp32 number (it is formed first).  A NaN scale or code makes the outputs of its rows NaN.
+ * codes and out 16-byte, scales 4-byte aligned.  m, n, k >= 1 (else INVALID_CONFIG); k below 2^23, m x k
+ * and n x k below 2^37, m x n below 2^40.  Errors: NULL, a bad out_dtype, k % 16, misalignment, sizes past the
+ * limits -> INVALID_ARG; a launch of 2^32 threads or more -> INVALID_CONFIG; else as qtip_moe_route. */
+qtip_status qtip_f8_matmul(const uint8_t* a_codes, const float* a_scales, int32_t m, const uint8_t* w_codes,
+                           const float* w_scales, int32_t n, int32_t k, void* out, int32_t out_dtype, void* stream);
+
+/* ---- e4m3 experts ----------------------------------------------------------------------------
+ * The expert matrices in e4m3, a fourth format, with e4m3 activations. */
+typedef struct qtip_f8_weights {
+  const uint8_t* codes_gate; /* [E][I][H] */
+  const float* scales_gate;  /* [E][I/128][H/128] */
+  const uint8_t* codes_up;   /* [E][I][H] */
+  const float* scales_up;    /* [E][I/128][H/128] */
+  const uint8_t* codes_down; /* [E][H][I] */
+  const float* scales_down;  /* [E][H/128][I/128] */
+} qtip_f8_weights;
+
+/* One expert pass over the pairs of a routed batch (qtip_moe_route, qtip_moe_gate_route), rows in pair
+ * order p = t k + j whatever the bins' order:
+ *   QTIP_F8_PASS_GATE_UP  a = x [n][H]:    out[p] = silu(x[t] Wg^T) * (x[t] Wu^T)   [n k][I]
+ *   QTIP_F8_PASS_DOWN     a = h [n k][I]:  out[p] = h[p] Wd^T                       [n k][H]
+ * with expert e's matrices for the pairs sorted_pair[offsets[e]] .. sorted_pair[offsets[e + 1] - 1], products as
+ * qtip_f8_matmul's.  out is bf16 or fp32, or, of the first pass, e4m3 (QTIP_OUT_E4M3): codes by the amax rule of the
+ * fp32 results, their scales in out_scales [n k][I/128] (else NULL), which the down pass takes as they are.
+ * Rows of out whose pair is in no bin are not written.  Offsets outside [0, n k] are held to it and pair ids
+ * outside [0, n k) skipped, so device-side garbage cannot reach memory out of bounds; of a pair that two
+ * bins name either's values remain.  Only the pass's own weights are read; the others may be NULL.  Codes and
+ * out 16-byte aligned, scales 4-byte aligned; the plan gives E, k, H, I and max_tokens; its rung, arm
+ * and variant do not matter.  Errors as qtip_moe_forward; a bad pass or out_dtype, out_scales missing or not
+ * wanted -> INVALID_ARG. */
+enum { QTIP_F8_PASS_GATE_UP = 0, QTIP_F8_PASS_DOWN = 1 };
+qtip_status qtip_f8_expert_matmul(qtip_moe_plan_t plan, int32_t pass, const qtip_f8_weights* w /*host struct*/,
+                                  const uint8_t* a_codes, const float* a_scales, const int32_t* offsets,
+                                  const int32_t* sorted_pair, int32_t n_tokens, void* out, int32_t out_dtype,
+                                  float* out_scales, void* stream);
+
+/* One MoE layer on e4m3 experts: route (through `gate`, or as qtip_moe_forward where it is NULL), bin, gate+up
+ * with h left in e4m3, down, combine.  x comes in e4m3 as qtip_f8_rms_norm or qtip_f8_quantize leave it: codes
+ * [n][H], scales [n][H/128].  y = h Wd^T in fp32; out[t] = sum_j w[t,j] y(t, j) in fp32, j ascending, cast to the
+ * plan's out_dtype.  Left-out slots add nothing.  workspace: qtip_f8_moe_workspace_bytes(plan) bytes,
+ * 256-byte aligned, contents need no initialisation; two calls, or replays of two captured graphs,
+ * that may overlap need one each.  Errors as qtip_moe_forward; a bad gate -> INVALID_ARG. */
+size_t qtip_f8_moe_workspace_bytes(qtip_moe_plan_t plan);
+qtip_status qtip_f8_moe_forward(qtip_moe_plan_t plan, const qtip_f8_weights* w /*host struct of device ptrs*/,
+                                const qtip_moe_gate* gate /*host struct or NULL*/, const uint8_t* x_codes,
+                                const float* x_scales, const float* logits, int32_t n_tokens, void* out,
+                                void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---- observability -----------------------------------------------------------------
  * qtip_moe_stats: copies the plan's launch counters (per arm, and per kernel configuration

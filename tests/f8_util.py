@@ -1,0 +1,85 @@
+"""Random e4m3 operands, error bounds and device calls for the e4m3 tests."""
+import numpy as np
+
+import trellis_quantized_moe_expert_amd as q
+from oracle import f8
+
+TYPE = {"bf16": q.QTIP_F8_BF16, "fp16": q.QTIP_F8_F16, "fp32": q.QTIP_F8_F32}
+RULE = {"amax": q.QTIP_F8_SCALE_AMAX, "pow2": q.QTIP_F8_SCALE_POW2}
+OUT = {"bf16": q.QTIP_OUT_BF16, "fp32": q.QTIP_OUT_F32, "e4m3": q.QTIP_OUT_E4M3}
+HALF = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11, "fp32": 2.0 ** -24}    # half a step, relative
+# half a step among the subnormal numbers: fp16 has steps of 2^-24 below 2^-14, the others of 2^-133 and 2^-149 below 2^-126
+LEAST = {"bf16": 2.0 ** -134, "fp16": 2.0 ** -25, "fp32": 2.0 ** -150}
+
+
+def dtype_of(name):
+    import torch
+    return {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}[name]
+
+
+def packed(rng, rows, cols, block_rows=1, lo=-3, hi=4):
+    """Uniform random finite codes, positive scales of every mantissa between 2^lo and 2^hi."""
+    codes = rng.integers(0, 127, (rows, cols)) + 128 * rng.integers(0, 2, (rows, cols))
+    scales = np.exp2(rng.uniform(lo, hi, (-(-rows // block_rows), -(-cols // 128)))).astype(np.float32)
+    return codes.astype(np.uint8), scales
+
+
+def sum_bound(a, w, blocks):
+    """Bound of |fp32 sum - exact| for sums over K of products a w: a block's 128 products are added in any order with
+    a last bit of 2^-23 each time (cut, not rounded); the product of the two scales, its product with the
+    block's sum and the sum over the blocks and over at most 16 waves round to 2^-24 each, all of at most
+    S = sum |a w|."""
+    return (127 * 2.0 ** -23 + (2 + blocks + 16) * 2.0 ** -24) * (np.abs(a) @ np.abs(w).T)
+
+
+def rounded(bound, ref, kind):
+    """The bound with the output's rounding (half a step) added."""
+    return bound + np.maximum(HALF[kind] * (np.abs(ref) + bound), LEAST[kind])
+
+
+def within(got, ref, lim):
+    err = np.abs(got - ref)
+    bad = np.argwhere(~(err <= lim))
+    assert len(bad) == 0, f"{len(bad)} of {err.size} off, first at {bad[0].tolist()}: {got[tuple(bad[0])]!r} for {ref[tuple(bad[0])]!r}"
+
+
+def norm_bound(cols):
+    """Relative bound of y: a thread adds at most cols / 1024 + 8 squares, then 6 + 16 sums of lanes and waves, each
+    within 2^-24; the root halves that; the mean, eps, root, quotient and two products round once each."""
+    return ((cols / 1024 + 8 + 22 + 1) / 2 + 6) * 2.0 ** -24
+
+
+def quantise(x, kind, rule, block_rows=1):
+    """codes, scales (numpy) of a 2-D device tensor (rows may be strided)."""
+    import torch
+    rows, cols = x.shape
+    codes = torch.full((rows, -(-cols // 16) * 16), 0xA5, dtype=torch.uint8, device="cuda:0")
+    scales = torch.full((-(-rows // block_rows), -(-cols // 128)), -7.0, device="cuda:0")
+    q.qtip_f8_quantize(x, TYPE[kind], rows, cols, x.stride(0), block_rows, RULE[rule], codes, scales)
+    torch.cuda.synchronize()
+    return codes.cpu().numpy(), scales.cpu().numpy()
+
+
+def same(got, want):
+    """Codes and scales equal bit for bit (any NaN is a NaN)."""
+    assert bool(np.array_equal(got[1], want[1], equal_nan=True)), np.argwhere(got[1] != want[1])[:4].tolist()
+    assert bool(np.array_equal(got[0], want[0])), np.argwhere(got[0] != want[0])[:4].tolist()
+
+
+def spread(scales, rows, cols, block_rows=1):
+    return scales.astype(np.float64)[np.arange(rows) // block_rows][:, np.arange(cols) // 128]
+
+
+def check_codes(codes, scales, y, lim):
+    """Codes and scales by the amax rule of numbers within lim of y."""
+    rows, cols = y.shape
+    s = spread(scales, rows, cols)
+    got = f8.TABLE[codes[:, :cols]] * s
+    step = np.maximum(2.0 ** -4 * (np.abs(y) + lim), s * 2.0 ** -10)
+    within(got, y, step + lim)
+    assert not codes[:, cols:].any()
+    for b in range(scales.shape[1]):
+        at = slice(128 * b, 128 * (b + 1))
+        top, off = np.abs(y[:, at]).max(1), lim[:, at].max(1)
+        want = np.maximum(top / 448, f8.TINY)
+        within(scales[:, b].astype(np.float64), want, off / 448 + 2.0 ** -24 * (want + off / 448))

@@ -30,6 +30,7 @@ QTIP_ACT_ROWS = 1
 QTIP_ACT_FRAGMENTS = 2
 QTIP_OUT_BF16 = 0
 QTIP_OUT_F32 = 1
+QTIP_OUT_E4M3 = 2
 QTIP_DEFAULT_DECODE_FLOOR_BITSHIFT = 7
 QTIP_DEFAULT_DECODE_FLOOR_LUT = 4
 QTIP_DECODE_REGIME_MAX_TOKENS = 8
@@ -48,6 +49,14 @@ QTIP_MX_SCALE_FLOOR = 0
 QTIP_MX_SCALE_NEAREST = 1
 QTIP_MX_PASS_GATE_UP = 0
 QTIP_MX_PASS_DOWN = 1
+QTIP_F8_BLOCK = 128
+QTIP_F8_BF16 = 0
+QTIP_F8_F16 = 1
+QTIP_F8_F32 = 2
+QTIP_F8_SCALE_AMAX = 0
+QTIP_F8_SCALE_POW2 = 1
+QTIP_F8_PASS_GATE_UP = 0
+QTIP_F8_PASS_DOWN = 1
 
 
 class qtip_moe_desc(ctypes.Structure):
@@ -102,6 +111,10 @@ class qtip_mx_weights(ctypes.Structure):
                 ("scales_up", ctypes.c_void_p), ("codes_down", ctypes.c_void_p), ("scales_down", ctypes.c_void_p)]
 
 
+class qtip_f8_weights(ctypes.Structure):
+    _fields_ = qtip_mx_weights._fields_
+
+
 class QtipError(RuntimeError):
     def __init__(self, fn: str, status: int, detail: str):
         self.status = status
@@ -152,6 +165,15 @@ _SIGS = {
     "qtip_mx_moe_workspace_bytes": (ctypes.c_size_t, [_P]),
     "qtip_mx_moe_forward": (_I32, [_P, ctypes.POINTER(qtip_mx_weights), ctypes.POINTER(qtip_moe_gate), _P, _P, _I32,
                                    _P, _P, ctypes.c_size_t, _P]),
+    "qtip_f8_quantize": (_I32, [_P, _I32, _I32, _I32, ctypes.c_int64, _I32, _I32, _P, _P, _P]),
+    "qtip_f8_rms_norm": (_I32, [_P, _I32, _I32, _I32, ctypes.c_int64, _P, ctypes.c_int64, _P, _P, _I32, ctypes.c_float,
+                                _I32, _P, _P, _P, _P]),
+    "qtip_f8_matmul": (_I32, [_P, _P, _I32, _P, _P, _I32, _I32, _P, _I32, _P]),
+    "qtip_f8_expert_matmul": (_I32, [_P, _I32, ctypes.POINTER(qtip_f8_weights), _P, _P, _P, _P, _I32, _P, _I32, _P,
+                                     _P]),
+    "qtip_f8_moe_workspace_bytes": (ctypes.c_size_t, [_P]),
+    "qtip_f8_moe_forward": (_I32, [_P, ctypes.POINTER(qtip_f8_weights), ctypes.POINTER(qtip_moe_gate), _P, _P, _P,
+                                   _I32, _P, _P, ctypes.c_size_t, _P]),
     "qtip_status_string": (ctypes.c_char_p, [_I32]),
     "qtip_last_error_detail": (ctypes.c_char_p, []),
 }
@@ -196,7 +218,7 @@ _get_device = None  # torch's current device and its stream's handle as plain ca
 _get_stream = None  # against 3.6 through torch.cuda.current_stream()
 _types = {}         # by kind of array (_KINDS): the element types it may have, the usual one first
 _KINDS = {"f": "float32", "i": "int32", "b": "bfloat16 int16 uint16", "h": "float16 int16 uint16",
-          "u": "uint8 int8 float4_e2m1fn_x2 float8_e8m0fnu"}  # 16-bit values may come as their bits
+          "u": "uint8 int8 float4_e2m1fn_x2 float8_e8m0fnu", "e": "uint8 int8 float8_e4m3fn"}  # 16-bit values may come as their bits
 
 
 def _find_torch() -> bool:
@@ -446,6 +468,16 @@ def make_mx_weights(codes_gate=None, scales_gate=None, codes_up=None, scales_up=
     return w
 
 
+def make_f8_weights(codes_gate=None, scales_gate=None, codes_up=None, scales_up=None, codes_down=None,
+                    scales_down=None) -> qtip_f8_weights:
+    """e4m3 expert weights; a pass reads only its own.  The struct keeps the tensors alive."""
+    arrays = (codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down)
+    w = qtip_f8_weights(*(_ptr(a) for a in arrays))
+    w.keep = arrays
+    w.seen = tuple(_seen("ef"[i & 1], a) for i, a in enumerate(arrays))
+    return w
+
+
 def _is_tensor(obj) -> bool:
     return obj is not None and obj.__class__ is not int and _find_torch() and isinstance(obj, _torch.Tensor)
 
@@ -514,17 +546,28 @@ def _layer(plan) -> tuple:
     return getattr(plan, "layer", None)
 
 
-def _check_mx_weights(fn: str, weights, layer, first: int, last: int) -> None:
-    """Arrays [first, last) of the struct's six: a matrix has H I values, two codes a byte, 32 to a scale."""
-    codes = layer[0] * layer[2] * layer[3] // 2 if layer else 0
+def _check_weights(fn: str, weights, codes: int, scales: int, first: int, last: int) -> None:
+    """Arrays [first, last) of the struct's six: codes and scales in turn, of at least so many bytes."""
     device = None
     for facts in getattr(weights, "seen", ())[first:last]:
         if facts is not None:
             device = _get_device() if device is None and not facts[0] else device
-            size = codes if first & 1 == 0 else codes // 16
+            size = codes if first & 1 == 0 else scales
             if facts[0] or facts[1] != device or facts[2] < size:
-                _check_seen(fn, qtip_mx_weights._fields_[first][0], facts, size)
+                _check_seen(fn, weights._fields_[first][0], facts, size)
         first += 1
+
+
+def _check_mx_weights(fn: str, weights, layer, first: int, last: int) -> None:
+    """A matrix has H I values, two codes a byte, 32 to a scale."""
+    codes = layer[0] * layer[2] * layer[3] // 2 if layer else 0
+    _check_weights(fn, weights, codes, codes // 16, first, last)
+
+
+def _check_f8_weights(fn: str, weights, layer, first: int, last: int) -> None:
+    """A matrix has H I values, a byte each, 128 x 128 to a scale."""
+    codes = layer[0] * layer[2] * layer[3] if layer else 0
+    _check_weights(fn, weights, codes, codes // 4096, first, last)
 
 
 def _check_bias(fn: str, gate, layer) -> None:
@@ -578,20 +621,26 @@ def qtip_moe_forward_gated(plan, weights: qtip_moe_weights, gate: qtip_moe_gate,
                                             p[3], workspace_bytes, _stream(stream)))
 
 
+def _check_rows(fn: str, name: str, kind: str, obj, rows: int, cols: int, row_stride: int) -> None:
+    """A tensor of a kind that holds `rows` rows of cols elements, row_stride apart: rows of a wider tensor are welcome."""
+    if not ((_torch is not None or _find_torch()) and isinstance(obj, _torch.Tensor)):
+        return
+    if obj.get_device() < 0 or obj.get_device() != _get_device():
+        _refuse(fn, name, "is not on the current device")
+    if kind != "." and obj.dtype not in _types[kind]:
+        _refuse(fn, name, f"has elements of {obj.dtype}, not of {_types[kind][0]}")
+    last = (rows - 1) * row_stride + cols
+    if obj.numel() < last or not obj.is_contiguous():
+        if obj.numel() == 0 or sum((n - 1) * st for n, st in zip(obj.shape, obj.stride())) < last - 1:
+            _refuse(fn, name, "is smaller than its rows")
+
+
 def qtip_mx_quantize(src, src_type, rows, cols, row_stride, scale_rule, codes, scales, values=None,
                      stream=None) -> None:
     fn = "qtip_mx_quantize"
     blocks = (cols + QTIP_MX_BLOCK - 1) // QTIP_MX_BLOCK
     kind, size = _SRC_KINDS.get(src_type, (".", 0))
-    if (_torch is not None or _find_torch()) and isinstance(src, _torch.Tensor):  # rows of a wider tensor are welcome
-        if src.get_device() < 0 or src.get_device() != _get_device():
-            _refuse(fn, "src", "is not on the current device")
-        if kind != "." and src.dtype not in _types[kind]:
-            _refuse(fn, "src", f"has elements of {src.dtype}, not of {_types[kind][0]}")
-        last = (rows - 1) * row_stride + cols
-        if src.numel() < last or not src.is_contiguous():
-            if src.numel() == 0 or sum((n - 1) * st for n, st in zip(src.shape, src.stride())) < last - 1:
-                _refuse(fn, "src", "is smaller than its rows")
+    _check_rows(fn, "src", kind, src, rows, cols, row_stride)
     sizes = 16 * rows * blocks, rows * blocks, rows * cols * size
     if values is None:
         p = _pointers(fn, "uu", ("codes", "scales"), (codes, scales), sizes)
@@ -638,6 +687,88 @@ def qtip_mx_moe_forward(plan, weights: qtip_mx_weights, gate, x_bf16, logits, n_
     _check_mx_weights(fn, weights, layer, 0, 6)
     _check(fn, lib().qtip_mx_moe_forward(plan, ctypes.byref(weights), None if gate is None else ctypes.byref(gate),
                                          p[0], p[1], n_tokens, p[2], p[3], workspace_bytes, _stream(stream)))
+
+
+def _f8_sizes(rows: int, cols: int, block_rows: int = 1) -> tuple:
+    """Bytes of the codes and of the scales of rows of cols values."""
+    return rows * ((cols + 15) // 16 * 16), 4 * ((rows + block_rows - 1) // block_rows) * ((cols + 127) // 128)
+
+
+def qtip_f8_quantize(src, src_type, rows, cols, row_stride, block_rows, scale_rule, codes, scales, stream=None) -> None:
+    fn = "qtip_f8_quantize"
+    _check_rows(fn, "src", _SRC_KINDS.get(src_type, (".", 0))[0], src, rows, cols, row_stride)
+    p = _pointers(fn, "ef", ("codes", "scales"), (codes, scales), _f8_sizes(rows, cols, max(block_rows, 1)))
+    _check(fn, lib().qtip_f8_quantize(_ptr(src), src_type, rows, cols, row_stride, block_rows, scale_rule, p[0], p[1],
+                                      _stream(stream)))
+
+
+def qtip_f8_rms_norm(x, type_, rows, cols, x_stride, residual, residual_stride, residual_out, weight, weight_type, eps,
+                     scale_rule, codes, scales, values=None, stream=None) -> None:
+    fn = "qtip_f8_rms_norm"
+    kind, size = _SRC_KINDS.get(type_, (".", 0))
+    w_kind, w_size = _SRC_KINDS.get(weight_type, (".", 0))
+    _check_rows(fn, "x", kind, x, rows, cols, x_stride)
+    if residual is not None or residual_out is not None:
+        _check_rows(fn, "residual", kind, residual, rows, cols, residual_stride)
+        _check_rows(fn, "residual_out", kind, residual_out, rows, cols, residual_stride)
+    sizes = w_size * cols, *_f8_sizes(rows, cols), size * rows * cols
+    if values is None:
+        p = _pointers(fn, w_kind + "ef", ("weight", "codes", "scales"), (weight, codes, scales), sizes[:3])
+        p.append(None)
+    else:
+        p = _pointers(fn, w_kind + "ef" + kind, ("weight", "codes", "scales", "values"), (weight, codes, scales, values),
+                      sizes)
+    _check(fn, lib().qtip_f8_rms_norm(_ptr(x), type_, rows, cols, x_stride, _ptr(residual), residual_stride,
+                                      _ptr(residual_out), p[0], weight_type, eps, scale_rule, p[1], p[2], p[3],
+                                      _stream(stream)))
+
+
+def qtip_f8_matmul(a_codes, a_scales, m, w_codes, w_scales, n, k, out, out_dtype, stream=None) -> None:
+    kind, size = _out_kind(out_dtype)
+    blocks = (k + 127) // 128 * 4
+    p = _pointers("qtip_f8_matmul", "efef" + kind, ("a_codes", "a_scales", "w_codes", "w_scales", "out"),
+                  (a_codes, a_scales, w_codes, w_scales, out),
+                  (m * k, m * blocks, n * k, (n + 127) // 128 * blocks, m * n * size))
+    _check("qtip_f8_matmul", lib().qtip_f8_matmul(p[0], p[1], m, p[2], p[3], n, k, p[4], out_dtype, _stream(stream)))
+
+
+def qtip_f8_expert_matmul(plan, pass_, weights: qtip_f8_weights, a_codes, a_scales, offsets, sorted_pair, n_tokens,
+                          out, out_dtype, out_scales=None, stream=None) -> None:
+    fn, layer = "qtip_f8_expert_matmul", _layer(plan)
+    E, k, H, I, _ = layer or (-1, 0, 0, 0, None)
+    pairs = n_tokens * k
+    gate_up = pass_ == QTIP_F8_PASS_GATE_UP
+    values, width = (n_tokens * H, I) if gate_up else (pairs * I, H)
+    kind, size = ("e", 1) if out_dtype == QTIP_OUT_E4M3 else _out_kind(out_dtype)
+    objs = a_codes, a_scales, offsets, sorted_pair, out
+    sizes = values, values // 32, 4 * E + 4, 4 * pairs, pairs * width * size
+    names = "a_codes", "a_scales", "offsets", "sorted_pair", "out", "out_scales"
+    if out_scales is None:
+        p = _pointers(fn, "efii" + kind, names, objs, sizes)
+        p.append(None)
+    else:
+        p = _pointers(fn, "efii" + kind + "f", names, (*objs, out_scales), (*sizes, pairs * width // 32))
+    _check_f8_weights(fn, weights, layer, 0 if gate_up else 4, 4 if gate_up else 6)
+    _check(fn, lib().qtip_f8_expert_matmul(plan, pass_, ctypes.byref(weights), p[0], p[1], p[2], p[3], n_tokens, p[4],
+                                           out_dtype, p[5], _stream(stream)))
+
+
+def qtip_f8_moe_workspace_bytes(plan) -> int:
+    return lib().qtip_f8_moe_workspace_bytes(plan)
+
+
+def qtip_f8_moe_forward(plan, weights: qtip_f8_weights, gate, x_codes, x_scales, logits, n_tokens, out, workspace,
+                        workspace_bytes, stream=None) -> None:
+    fn, layer = "qtip_f8_moe_forward", _layer(plan)
+    E, _, H, _, out_dtype = layer or (0, 0, 0, 0, None)
+    kind, size = (".", 0) if out_dtype is None else _out_kind(out_dtype)
+    p = _pointers(fn, "eff" + kind + ".", ("x_codes", "x_scales", "logits", "out", "workspace"),
+                  (x_codes, x_scales, logits, out, workspace),
+                  (n_tokens * H, n_tokens * H // 32, 4 * n_tokens * E, size * n_tokens * H, workspace_bytes))
+    _check_bias(fn, gate, layer)
+    _check_f8_weights(fn, weights, layer, 0, 6)
+    _check(fn, lib().qtip_f8_moe_forward(plan, ctypes.byref(weights), None if gate is None else ctypes.byref(gate),
+                                         p[0], p[1], p[2], n_tokens, p[3], p[4], workspace_bytes, _stream(stream)))
 
 
 def raw_status(fn_name: str, *args) -> int:

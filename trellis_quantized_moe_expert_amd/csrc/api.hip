@@ -17,6 +17,7 @@
 #include <vector>
 
 #include "../../include/qtip_moe.h"
+#include "f8_internal.h"
 #include "fill_predicate.h"
 #include "mx_internal.h"
 #include "qtip_internal.h"
@@ -1129,6 +1130,93 @@ MxWsLayout mx_ws_layout(const qtip_moe_desc& d) {
   return L;
 }
 
+// The experts, weights and bins of a layer's tokens, through a gate where one is given (already checked).
+qtip_status route_layer(qtip_moe_plan_s* plan, const qtip_moe_gate* gate, const float* logits, int32_t n_tokens,
+                        int32_t* topk_idx, float* topk_w, const GateBins& bins, hipStream_t st) {
+  hipError_t e;
+  if (gate) {
+    e = launch_gate(gate_params(plan, gate, logits, n_tokens, topk_idx, topk_w), &bins, st);
+    if (e != hipSuccess) return hip_fail(e, "gate launch");
+  } else {
+    e = launch_route_topk(logits, 1, n_tokens, plan->d.num_experts, plan->d.top_k, topk_idx, topk_w, st);
+    if (e != hipSuccess) return hip_fail(e, "route_topk launch");
+    GateParams g{};
+    g.n = n_tokens;
+    g.E = plan->d.num_experts;
+    g.k = plan->d.top_k;
+    g.topk_idx = topk_idx;
+    e = launch_gate_bins(g, bins, st);
+    if (e != hipSuccess) return hip_fail(e, "bin launch");
+    plan->stats.route_launches++;
+  }
+  plan->stats.route_launches++;
+  return QTIP_OK;
+}
+
+// ---- e4m3 experts -----------------------------------------------------------------------------
+bool f8_type(int32_t t) { return t == QTIP_F8_BF16 || t == QTIP_F8_F16 || t == QTIP_F8_F32; }
+uintptr_t f8_type_mask(int32_t t) { return t == QTIP_F8_F32 ? 3 : 1; }
+bool f8_aligned(const void* codes, const void* scales) { return mx_aligned(codes, scales); }
+
+qtip_status check_f8_pass(int32_t pass, const qtip_f8_weights* w) {
+  if (pass != QTIP_F8_PASS_GATE_UP && pass != QTIP_F8_PASS_DOWN) return fail(QTIP_ERR_INVALID_ARG, "unknown pass");
+  const bool gu = pass == QTIP_F8_PASS_GATE_UP;
+  const void* codes[2] = {gu ? w->codes_gate : w->codes_down, gu ? w->codes_up : w->codes_down};
+  const void* scales[2] = {gu ? w->scales_gate : w->scales_down, gu ? w->scales_up : w->scales_down};
+  for (int i = 0; i < 2; ++i) {
+    if (!codes[i] || !scales[i]) return fail(QTIP_ERR_INVALID_ARG, "NULL weight pointer");
+    if (!f8_aligned(codes[i], scales[i]))
+      return fail(QTIP_ERR_INVALID_ARG, "weight codes must be 16-byte aligned, scales 4-byte aligned");
+  }
+  return QTIP_OK;
+}
+
+F8MatmulParams f8_pass_params(const qtip_moe_plan_s* plan, int32_t pass, const qtip_f8_weights* w,
+                              const uint8_t* a_codes, const float* a_scales, const int32_t* offsets,
+                              const int32_t* sorted_pair, int32_t n_tokens, void* out, int32_t out_dtype,
+                              float* out_scales) {
+  const bool gu = pass == QTIP_F8_PASS_GATE_UP;
+  F8MatmulParams p{};
+  p.a = a_codes;
+  p.a_scale = a_scales;
+  p.w0 = gu ? w->codes_gate : w->codes_down;
+  p.w0_scale = gu ? w->scales_gate : w->scales_down;
+  p.w1 = gu ? w->codes_up : nullptr;
+  p.w1_scale = gu ? w->scales_up : nullptr;
+  p.offsets = offsets;
+  p.sorted_pair = sorted_pair;
+  p.E = plan->d.num_experts;
+  p.a_div = gu ? plan->d.top_k : 1;
+  p.m = n_tokens * plan->d.top_k;
+  p.n = gu ? plan->d.inter : plan->d.hidden;
+  p.k = gu ? plan->d.hidden : plan->d.inter;
+  p.out = out;
+  p.out_bf16 = out_dtype == QTIP_OUT_BF16;
+  p.out_scale = out_scales;
+  return p;
+}
+
+struct F8WsLayout {
+  size_t topk_idx, topk_w, counts, offsets, sorted_pair, hist, h_codes, h_scales, y, total;
+};
+
+F8WsLayout f8_ws_layout(const qtip_moe_desc& d) {
+  const size_t P = (size_t)d.max_tokens * d.top_k;
+  F8WsLayout L{};
+  size_t o = 0;
+  L.topk_idx = o;     o = align256(o + P * 4);
+  L.topk_w = o;       o = align256(o + P * 4);
+  L.counts = o;       o = align256(o + (size_t)d.num_experts * 4);
+  L.offsets = o;      o = align256(o + ((size_t)d.num_experts + 1) * 4);
+  L.sorted_pair = o;  o = align256(o + P * 4);
+  L.hist = o;         o = align256(o + (size_t)kGateMaxBlocks * d.num_experts * 4);
+  L.h_codes = o;      o = align256(o + P * d.inter);
+  L.h_scales = o;     o = align256(o + P * (d.inter / kF8Block) * 4);
+  L.y = o;            o = align256(o + P * d.hidden * 4);
+  L.total = o;
+  return L;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1544,28 +1632,13 @@ qtip_status qtip_mx_moe_forward(qtip_moe_plan_t plan, const qtip_mx_weights* w, 
   float* y = reinterpret_cast<float*>(ws + L.y);
   const int32_t P = n_tokens * d.top_k;
 
-  hipError_t e;
   GateBins bins{};
   bins.counts = counts;
   bins.offsets = offsets;
   bins.sorted_pair = sorted_pair;
   bins.hist = reinterpret_cast<int32_t*>(ws + L.hist);
-  if (gate) {
-    e = launch_gate(gate_params(plan, gate, logits, n_tokens, topk_idx, topk_w), &bins, st);
-    if (e != hipSuccess) return hip_fail(e, "gate launch");
-  } else {
-    e = launch_route_topk(logits, 1, n_tokens, d.num_experts, d.top_k, topk_idx, topk_w, st);
-    if (e != hipSuccess) return hip_fail(e, "route_topk launch");
-    GateParams g{};
-    g.n = n_tokens;
-    g.E = d.num_experts;
-    g.k = d.top_k;
-    g.topk_idx = topk_idx;
-    e = launch_gate_bins(g, bins, st);
-    if (e != hipSuccess) return hip_fail(e, "bin launch");
-    plan->stats.route_launches++;
-  }
-  plan->stats.route_launches++;
+  if ((s = route_layer(plan, gate, logits, n_tokens, topk_idx, topk_w, bins, st)) != QTIP_OK) return s;
+  hipError_t e;
   MxQuantParams q{};
   q.src = x_bf16;
   q.row_stride = d.hidden;
@@ -1592,6 +1665,199 @@ qtip_status qtip_mx_moe_forward(qtip_moe_plan_t plan, const qtip_mx_weights* w, 
   e = launch_mx_matmul(mx_pass_params(plan, QTIP_MX_PASS_DOWN, w, h_codes, h_scales, offsets, sorted_pair, n_tokens, y,
                                       QTIP_OUT_F32), st);
   if (e != hipSuccess) return hip_fail(e, "MXFP4 down launch");
+  e = launch_combine_chosen(y, topk_w, topk_idx, d.num_experts, n_tokens, d.top_k, d.hidden, out,
+                            d.out_dtype == QTIP_OUT_BF16, st);
+  if (e != hipSuccess) return hip_fail(e, "combine launch");
+  plan->stats.combine_launches++;
+  return QTIP_OK;
+}
+
+// ---- e4m3 -------------------------------------------------------------------------------------
+
+qtip_status qtip_f8_quantize(const void* src, int32_t src_type, int32_t rows, int32_t cols, int64_t row_stride,
+                             int32_t block_rows, int32_t scale_rule, uint8_t* codes, float* scales, void* stream) {
+  g_detail.clear();
+  if (!src || !codes || !scales) return fail(QTIP_ERR_INVALID_ARG, "NULL argument");
+  if (!f8_type(src_type)) return fail(QTIP_ERR_INVALID_ARG, "unknown src_type");
+  if (scale_rule != QTIP_F8_SCALE_AMAX && scale_rule != QTIP_F8_SCALE_POW2)
+    return fail(QTIP_ERR_INVALID_ARG, "unknown scale_rule");
+  if (block_rows != 1 && block_rows != kF8Block) return fail(QTIP_ERR_INVALID_ARG, "block_rows must be 1 or 128");
+  if (rows < 1 || cols < 1) return fail(QTIP_ERR_INVALID_CONFIG, "rows and cols must be >= 1 (an empty launch is an error)");
+  if (row_stride < cols || row_stride >= ((int64_t)1 << 40))
+    return fail(QTIP_ERR_INVALID_ARG, "row_stride must be at least cols and below 2^40");
+  // 16 threads a block of a row, 256 a block of 128 rows; whole workgroups, below 2^32 threads
+  const int64_t blocks = ((int64_t)cols + kF8Block - 1) / kF8Block;
+  if (block_rows == 1 ? rows * blocks > ((int64_t)1 << 28) - 16
+                      : ((int64_t)rows + kF8Block - 1) / kF8Block * blocks >= ((int64_t)1 << 24))
+    return fail(QTIP_ERR_INVALID_ARG, "too many blocks: at most 2^28 - 16 of 128 values, 2^24 - 1 of 128 x 128");
+  if ((reinterpret_cast<uintptr_t>(src) & f8_type_mask(src_type)) || !f8_aligned(codes, scales))
+    return fail(QTIP_ERR_INVALID_ARG, "src must be aligned to its type, codes to 16 bytes, scales to 4");
+  const hipStream_t st = (hipStream_t)stream;
+  int dev = 0;
+  const qtip_status s = ensure_current(st, &dev);
+  if (s != QTIP_OK) return s;
+  F8QuantParams p{};
+  p.src = src;
+  p.row_stride = row_stride;
+  p.rows = rows;
+  p.cols = cols;
+  p.type = src_type;
+  p.block_rows = block_rows;
+  p.pow2 = scale_rule == QTIP_F8_SCALE_POW2;
+  p.codes = codes;
+  p.scales = scales;
+  const hipError_t e = launch_f8_quantize(p, st);
+  return e == hipSuccess ? QTIP_OK : hip_fail(e, "e4m3 quantize launch");
+}
+
+qtip_status qtip_f8_rms_norm(const void* x, int32_t type, int32_t rows, int32_t cols, int64_t x_stride,
+                             const void* residual, int64_t residual_stride, void* residual_out, const void* weight,
+                             int32_t weight_type, float eps, int32_t scale_rule, uint8_t* codes, float* scales,
+                             void* values, void* stream) {
+  g_detail.clear();
+  if (!x || !weight || !codes || !scales) return fail(QTIP_ERR_INVALID_ARG, "NULL argument");
+  if (!residual != !residual_out)
+    return fail(QTIP_ERR_INVALID_ARG, "residual and residual_out must both be given or both be NULL");
+  if (!f8_type(type) || !f8_type(weight_type)) return fail(QTIP_ERR_INVALID_ARG, "unknown type or weight_type");
+  if (scale_rule != QTIP_F8_SCALE_AMAX && scale_rule != QTIP_F8_SCALE_POW2)
+    return fail(QTIP_ERR_INVALID_ARG, "unknown scale_rule");
+  if (!std::isfinite(eps) || eps < 0) return fail(QTIP_ERR_INVALID_ARG, "eps must be finite and at least 0");
+  if (rows < 1 || cols < 1) return fail(QTIP_ERR_INVALID_CONFIG, "rows and cols must be >= 1 (an empty launch is an error)");
+  // a workgroup of at most 1024 threads a row, below 2^32 threads
+  if (rows >= 1 << 22 || cols > 1 << 30) return fail(QTIP_ERR_INVALID_ARG, "rows must be below 2^22, cols at most 2^30");
+  if (x_stride < cols || x_stride >= ((int64_t)1 << 40) ||
+      (residual && (residual_stride < cols || residual_stride >= ((int64_t)1 << 40))))
+    return fail(QTIP_ERR_INVALID_ARG, "strides must be at least cols and below 2^40");
+  const uintptr_t mask = f8_type_mask(type);
+  if ((reinterpret_cast<uintptr_t>(x) & mask) || (reinterpret_cast<uintptr_t>(residual) & mask) ||
+      (reinterpret_cast<uintptr_t>(residual_out) & mask) ||
+      (reinterpret_cast<uintptr_t>(weight) & f8_type_mask(weight_type)) || !f8_aligned(codes, scales) ||
+      (reinterpret_cast<uintptr_t>(values) & 15))
+    return fail(QTIP_ERR_INVALID_ARG, "inputs must be aligned to their type, codes and values to 16 bytes, scales to 4");
+  const hipStream_t st = (hipStream_t)stream;
+  int dev = 0;
+  const qtip_status s = ensure_current(st, &dev);
+  if (s != QTIP_OK) return s;
+  F8NormParams p{};
+  p.x = x;
+  p.x_stride = x_stride;
+  p.residual = residual;
+  p.residual_out = residual_out;
+  p.residual_stride = residual_stride;
+  p.weight = weight;
+  p.rows = rows;
+  p.cols = cols;
+  p.type = type;
+  p.weight_type = weight_type;
+  p.eps = eps;
+  p.pow2 = scale_rule == QTIP_F8_SCALE_POW2;
+  p.codes = codes;
+  p.scales = scales;
+  p.values = values;
+  const hipError_t e = launch_f8_rms_norm(p, st);
+  return e == hipSuccess ? QTIP_OK : hip_fail(e, "RMS norm launch");
+}
+
+qtip_status qtip_f8_matmul(const uint8_t* a_codes, const float* a_scales, int32_t m, const uint8_t* w_codes,
+                           const float* w_scales, int32_t n, int32_t k, void* out, int32_t out_dtype, void* stream) {
+  g_detail.clear();
+  if (!a_codes || !a_scales || !w_codes || !w_scales || !out) return fail(QTIP_ERR_INVALID_ARG, "NULL argument");
+  if (out_dtype != QTIP_OUT_BF16 && out_dtype != QTIP_OUT_F32) return fail(QTIP_ERR_INVALID_ARG, "unknown out_dtype");
+  if (m < 1 || n < 1 || k < 1) return fail(QTIP_ERR_INVALID_CONFIG, "m, n and k must be >= 1 (an empty launch is an error)");
+  if (k % 16) return fail(QTIP_ERR_INVALID_ARG, "k must be a multiple of 16");
+  if (k >= 1 << 23 || (int64_t)m * k >= ((int64_t)1 << 37) || (int64_t)n * k >= ((int64_t)1 << 37) ||
+      (int64_t)m * n >= ((int64_t)1 << 40))
+    return fail(QTIP_ERR_INVALID_ARG, "k must be below 2^23, m * k and n * k below 2^37, m * n below 2^40");
+  if (!f8_aligned(a_codes, a_scales) || !f8_aligned(w_codes, w_scales) || (reinterpret_cast<uintptr_t>(out) & 15))
+    return fail(QTIP_ERR_INVALID_ARG, "codes and out must be 16-byte aligned, scales 4-byte aligned");
+  F8MatmulParams p{};
+  p.a = a_codes;
+  p.a_scale = a_scales;
+  p.w0 = w_codes;
+  p.w0_scale = w_scales;
+  p.E = 1;
+  p.a_div = 1;
+  p.m = m;
+  p.n = n;
+  p.k = k;
+  p.out = out;
+  p.out_bf16 = out_dtype == QTIP_OUT_BF16;
+  if (!f8_matmul_fits(p)) return fail(QTIP_ERR_INVALID_CONFIG, "m and n need a launch of 2^32 threads or more");
+  const hipStream_t st = (hipStream_t)stream;
+  int dev = 0;
+  const qtip_status s = ensure_current(st, &dev);
+  if (s != QTIP_OK) return s;
+  const hipError_t e = launch_f8_matmul(p, st);
+  return e == hipSuccess ? QTIP_OK : hip_fail(e, "e4m3 matmul launch");
+}
+
+qtip_status qtip_f8_expert_matmul(qtip_moe_plan_t plan, int32_t pass, const qtip_f8_weights* w,
+                                  const uint8_t* a_codes, const float* a_scales, const int32_t* offsets,
+                                  const int32_t* sorted_pair, int32_t n_tokens, void* out, int32_t out_dtype,
+                                  float* out_scales, void* stream) {
+  g_detail.clear();
+  if (!plan || !w || !a_codes || !a_scales || !offsets || !sorted_pair || !out)
+    return fail(QTIP_ERR_INVALID_ARG, "NULL argument");
+  qtip_status s = check_f8_pass(pass, w);
+  if (s != QTIP_OK) return s;
+  if (out_dtype != QTIP_OUT_BF16 && out_dtype != QTIP_OUT_F32 &&
+      (out_dtype != QTIP_OUT_E4M3 || pass != QTIP_F8_PASS_GATE_UP))
+    return fail(QTIP_ERR_INVALID_ARG, "unknown out_dtype (e4m3 is of the gate+up pass only)");
+  if ((out_dtype == QTIP_OUT_E4M3) != (out_scales != nullptr))
+    return fail(QTIP_ERR_INVALID_ARG, "out_scales must be given with QTIP_OUT_E4M3 and be NULL otherwise");
+  if (!f8_aligned(a_codes, a_scales) || !f8_aligned(out, out_scales))
+    return fail(QTIP_ERR_INVALID_ARG, "codes and out must be 16-byte aligned, scales 4-byte aligned");
+  if (n_tokens <= 0 || n_tokens > plan->d.max_tokens)
+    return fail(QTIP_ERR_INVALID_CONFIG, "n_tokens must be in [1, max_tokens] (an empty launch is an error)");
+  const hipStream_t st = (hipStream_t)stream;
+  int dev = 0;
+  if ((s = ensure_device(plan, st, &dev)) != QTIP_OK) return s;
+  const hipError_t e = launch_f8_matmul(f8_pass_params(plan, pass, w, a_codes, a_scales, offsets, sorted_pair, n_tokens,
+                                                       out, out_dtype, out_scales), st);
+  return e == hipSuccess ? QTIP_OK : hip_fail(e, "e4m3 expert launch");
+}
+
+size_t qtip_f8_moe_workspace_bytes(qtip_moe_plan_t plan) { return plan ? f8_ws_layout(plan->d).total : 0; }
+
+qtip_status qtip_f8_moe_forward(qtip_moe_plan_t plan, const qtip_f8_weights* w, const qtip_moe_gate* gate,
+                                const uint8_t* x_codes, const float* x_scales, const float* logits, int32_t n_tokens,
+                                void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  g_detail.clear();
+  if (!plan || !w || !x_codes || !x_scales || !logits || !out || !workspace)
+    return fail(QTIP_ERR_INVALID_ARG, "NULL argument");
+  qtip_status s;
+  if ((s = check_f8_pass(QTIP_F8_PASS_GATE_UP, w)) != QTIP_OK) return s;
+  if ((s = check_f8_pass(QTIP_F8_PASS_DOWN, w)) != QTIP_OK) return s;
+  if (gate && (s = check_gate(plan, gate)) != QTIP_OK) return s;
+  if (!f8_aligned(x_codes, x_scales) || (reinterpret_cast<uintptr_t>(out) & 15))
+    return fail(QTIP_ERR_INVALID_ARG, "x_codes and out must be 16-byte aligned, x_scales 4-byte aligned");
+  if (n_tokens <= 0 || n_tokens > plan->d.max_tokens)
+    return fail(QTIP_ERR_INVALID_CONFIG, "n_tokens must be in [1, max_tokens] (an empty launch is an error)");
+  const qtip_moe_desc& d = plan->d;
+  const F8WsLayout L = f8_ws_layout(d);
+  if (workspace_bytes < L.total || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return fail(QTIP_ERR_INVALID_ARG, "workspace too small or not 256-byte aligned");
+  const hipStream_t st = (hipStream_t)stream;
+  int dev = 0;
+  if ((s = ensure_device(plan, st, &dev)) != QTIP_OK) return s;
+  char* ws = reinterpret_cast<char*>(workspace);
+  int32_t* topk_idx = reinterpret_cast<int32_t*>(ws + L.topk_idx);
+  float* topk_w = reinterpret_cast<float*>(ws + L.topk_w);
+  uint8_t* h_codes = reinterpret_cast<uint8_t*>(ws + L.h_codes);
+  float* h_scales = reinterpret_cast<float*>(ws + L.h_scales);
+  float* y = reinterpret_cast<float*>(ws + L.y);
+  GateBins bins{};
+  bins.counts = reinterpret_cast<int32_t*>(ws + L.counts);
+  bins.offsets = reinterpret_cast<int32_t*>(ws + L.offsets);
+  bins.sorted_pair = reinterpret_cast<int32_t*>(ws + L.sorted_pair);
+  bins.hist = reinterpret_cast<int32_t*>(ws + L.hist);
+  if ((s = route_layer(plan, gate, logits, n_tokens, topk_idx, topk_w, bins, st)) != QTIP_OK) return s;
+  hipError_t e = launch_f8_matmul(f8_pass_params(plan, QTIP_F8_PASS_GATE_UP, w, x_codes, x_scales, bins.offsets,
+                                                 bins.sorted_pair, n_tokens, h_codes, QTIP_OUT_E4M3, h_scales), st);
+  if (e != hipSuccess) return hip_fail(e, "e4m3 gate/up launch");
+  e = launch_f8_matmul(f8_pass_params(plan, QTIP_F8_PASS_DOWN, w, h_codes, h_scales, bins.offsets, bins.sorted_pair,
+                                      n_tokens, y, QTIP_OUT_F32, nullptr), st);
+  if (e != hipSuccess) return hip_fail(e, "e4m3 down launch");
   e = launch_combine_chosen(y, topk_w, topk_idx, d.num_experts, n_tokens, d.top_k, d.hidden, out,
                             d.out_dtype == QTIP_OUT_BF16, st);
   if (e != hipSuccess) return hip_fail(e, "combine launch");
