@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 import trellis_quantized_moe_expert_amd as q
-from f8_util import (OUT, RULE, TYPE, check_codes, dtype_of, norm_bound, packed, quantise, rounded, same, sum_bound,
+from f8_util import (OUT, RULE, TYPE, check_codes, dtype_of, eight_bound, norm_bound, packed, quantise, rounded, same, sum_bound,
                      within)
 from gpu_util import say
 from mx_util import bins_of
@@ -212,7 +212,8 @@ def check_product(a, w, kind):
     k = a[0].shape[1]
     av, wv = f8.decode(*a), f8.decode(*w, 128)
     ref = av @ wv.T
-    within(product(a, w, k, kind), ref, rounded(sum_bound(av, wv, -(-k // 128)), ref, kind))
+    lim = sum_bound(av, wv, -(-k // 128)) + (eight_bound(av, wv) if kind == "bf16" else 0.0)
+    within(product(a, w, k, kind), ref, rounded(lim, ref, kind))
 
 
 SIZES = [(1, 1, 16), (1, 16, 128), (1, 4096, 512), (2, 17, 144), (3, 100, 560), (15, 33, 1040), (16, 16, 2048),
@@ -326,8 +327,9 @@ class Experts:
         codes, scales = self.w[name]
         return f8.decode(codes[e * rows:(e + 1) * rows], scales[e * rows // 128:(e + 1) * rows // 128], 128)
 
-    def reference(self, part):
+    def reference(self, part, kind):
         """(rows, results, bounds) of each expert with pairs."""
+        bound = lambda a, w: sum_bound(a, w, a.shape[1] // 128) + (eight_bound(a, w) if kind == "bf16" else 0.0)
         flat = self.idx.reshape(-1)
         for e in range(self.E):
             pairs = np.flatnonzero(flat == e)
@@ -339,15 +341,15 @@ class Experts:
                 gr, ur = a @ g.T, a @ u.T
                 ref = mx.silu(gr) * ur
                 # silu itself: exp, add, reciprocal and two products in fp32, a few steps of 2^-24 relative
-                lim = mx.swiglu_bound(gr, ur, sum_bound(a, g, self.H // 128), sum_bound(a, u, self.H // 128))
+                lim = mx.swiglu_bound(gr, ur, bound(a, g), bound(a, u))
                 yield pairs, ref, lim + 8 * 2.0 ** -24 * np.abs(ref)
             else:
                 a, d = f8.decode(*self.h)[pairs], self.matrix("down", e)
-                yield pairs, a @ d.T, sum_bound(a, d, self.I // 128)
+                yield pairs, a @ d.T, bound(a, d)
 
     def check(self, part, kind):
         got = self.run(part, kind)
-        for pairs, ref, lim in self.reference(part):
+        for pairs, ref, lim in self.reference(part, kind):
             if kind == "e4m3":
                 check_codes(got[0][pairs], got[1][pairs], ref, lim)
                 continue

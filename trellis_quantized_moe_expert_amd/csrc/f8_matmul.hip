@@ -26,6 +26,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 // A lane's 32 values of a block, widened.
 struct Wide {
   bf16x8 v[4];
+  Wide() = default;
   __device__ explicit Wide(const i32x4 (&c)[2]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -289,6 +290,280 @@ __global__ __launch_bounds__(S * 512) void direct_pair_kernel(F8MatmulParams p) 
   }
 }
 
+// ---- the tiled kernel -----------------------------------------------------------------------
+// A workgroup of WM x WN waves computes BM activation rows by BN weight rows (with two matrices BN / 2 rows of each, so
+// that a wave holds both factors of its outputs).  A stage is one block of 128 inputs: it goes from memory to LDS
+// without passing registers, NST - 1 stages ahead of the one being multiplied; rows and chunks past the operands'
+// ends are given an offset past the buffer's range, for which the load writes zeros.
+//
+// A row's eight 16-byte chunks are stored so that the 16 lanes of an LDS read phase touch 16 different 16-byte
+// columns of the banks: see place_of.  The activations' scales of a stage go to LDS beside it, a dword a row; a wave's
+// weight rows lie in one 128-row block of a matrix, and its scales of 64 stages stay in a register, a lane each.
+
+// Place of chunk c in LDS row `row`, in 16-byte units, and the other way round.
+__device__ inline int place_of(int row, int c) { return c ^ ((row >> 1) & 7); }
+
+// A lane's chunks of an LDS row, for the 8-bit instruction or widened.
+template <bool EXACT> struct Fragment {
+  Wide v;
+  Fragment() = default;
+  __device__ explicit Fragment(const i32x4 (&c)[2]) : v(c) {}
+  static __device__ f32x4 multiply(const Fragment& w, const Fragment& a) { return multiply_block(w.v, a.v); }
+};
+template <> struct Fragment<false> {
+  i32x8 v;
+  Fragment() = default;
+  __device__ explicit Fragment(const i32x4 (&c)[2])
+      : v{c[0][0], c[0][1], c[0][2], c[0][3], c[1][0], c[1][1], c[1][2], c[1][3]} {}
+  static __device__ f32x4 multiply(const Fragment& w, const Fragment& a) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, a.v, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+  }
+};
+
+template <int BM, int BN, int WM, int WN, int NST, int HALVES, bool EXACT>
+__global__ __launch_bounds__(WM * WN * 64) void tiled_kernel(F8MatmulParams p, int tiles, int row_blocks) {
+  constexpr int kThreads = WM * WN * 64;
+  constexpr int kRows = BM + BN;                      // rows of a stage: activations, then weights
+  constexpr int kChunks = kF8Block / 16;              // of a row in a stage
+  constexpr int kLoads = kRows * kChunks / kThreads;  // 16-byte loads of a thread and stage
+  constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
+  constexpr int FH = FN / HALVES;                     // fragments of one matrix
+  constexpr bool kPair = FH % 2 == 0;                 // two fragments side by side: 8 outputs in a lane
+  static_assert(kRows * kChunks % kThreads == 0 && BM * kChunks % kThreads == 0, "a load is of one operand");
+  static_assert(BM <= kThreads && FH >= 1 && FH * 16 <= kF8Block && (NST == 2 || NST == 4), "");
+  constexpr int kCodes = kRows * kF8Block, kStage = kCodes + kThreads * 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t c0[kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t c1[kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t c2[NST > 2 ? kStage : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t c3[NST > 2 ? kStage : 16];
+  __shared__ uint32_t tops[HALVES == 2 ? BM : 1][WN];
+
+  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wv / WN, wn = wv % WN;
+  const int j = lane & 15, g = lane >> 4;
+
+  int tile, rb;
+  tile_of_block(p, tiles, row_blocks, (int)blockIdx.x, tile, rb);
+  if (tile >= tiles) return;
+  int expert = 0, start = tile * BM, len = min(BM, p.m - start);
+  if (p.offsets && !find_tile(p.offsets, p.E, p.m, BM, tile, expert, start, len)) return;
+  const int n0 = rb * (BN / HALVES);
+  const int blocks = (p.k + kF8Block - 1) / kF8Block;
+
+  // Row `r` of the weight part of a stage: its matrix and row.  Neighbouring fragments of a wave
+  // take rows 8i .. 8i + 3 and 8i + 4 .. 8i + 7, so that a lane's outputs of both are 8 in a row.
+  auto weight_row = [&](int r, int& half) {
+    const int w = r / (BN / WN), in = r % (BN / WN);
+    half = HALVES == 2 ? in / (FH * 16) : 0;
+    const int q = in % (FH * 16);
+    int col = q;
+    if (kPair) col = (q / 32) * 32 + 8 * (q % 16 / 4) + 4 * (q / 16 % 2) + q % 4;
+    return n0 + w * (FH * 16) + col;
+  };
+  // Activation row of tile place i, or -1.
+  auto act_row = [&](int i) {
+    const int r = tile_row(p, start, len, i);
+    return r < 0 ? -1 : (p.offsets ? r / p.a_div : r);
+  };
+
+  // Dense activations are addressed from the tile's first row, gathered ones from row 0 (a plan keeps them under
+  // 2^30 bytes); their scales, a thirty-second of the codes, likewise.
+  const int a_base = p.offsets ? 0 : start;
+  const size_t w_base = ((size_t)expert * p.n + n0) * p.k;
+  const __amdgpu_buffer_rsrc_t ra = product_rsrc(p.a + (size_t)a_base * p.k);
+  const __amdgpu_buffer_rsrc_t rs = product_rsrc(p.a_scale + (size_t)a_base * blocks);
+  const __amdgpu_buffer_rsrc_t rw0 = product_rsrc(p.w0 + w_base);
+  const __amdgpu_buffer_rsrc_t rw1 = product_rsrc(HALVES == 2 ? p.w1 + w_base : p.w0 + w_base);
+
+  // Load i of a thread: LDS row and first byte in the row of the stage.
+  auto load_at = [&](int i, int& r, int& byte) {
+    const int slot = i * kThreads + tid;
+    r = slot / kChunks;
+    byte = place_of(r, slot % kChunks) * 16;  // its own inverse
+  };
+  uint32_t off[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    int r, byte;
+    load_at(i, r, byte);
+    if (i * kThreads < BM * kChunks) {
+      const int row = act_row(r);
+      off[i] = row < 0 ? kNoRow : (uint32_t)((size_t)(row - a_base) * p.k) + byte;
+    } else {
+      int half;
+      const int row = weight_row(r - BM, half);
+      off[i] = row < p.n ? (uint32_t)((size_t)(row - n0) * p.k) + byte : kNoRow;
+    }
+  }
+  const int scale_row = tid < BM ? act_row(tid) : -1;
+  const uint32_t scale_off = scale_row < 0 ? kNoRow : (uint32_t)((size_t)(scale_row - a_base) * blocks * 4);
+  auto issue = [&](uint8_t* dst, int s) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      // chunks past the row's end, and stages past the last
+      int r, byte;
+      load_at(i, r, byte);
+      const uint32_t o = s * kF8Block + byte < p.k ? off[i] : kNoRow;
+      const int so = min(s, blocks) * kF8Block;
+      lds_void* at = (lds_void*)(dst + (i * kThreads + wv * 64) * 16);
+      if (i * kThreads < BM * kChunks) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, at, 16, o, so, 0, 0);
+      } else {
+        int half = 0;  // a wave's load is of rows of one fragment, so of one matrix
+        if (HALVES == 2) weight_row((i * kThreads + wv * 64) / kChunks - BM, half);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(half ? rw1 : rw0, at, 16, o, so, 0, 0);
+      }
+    }
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(dst + kCodes + wv * 256), 4, s < blocks ? scale_off : kNoRow,
+                                             min(s, blocks) * 4, 0, 0);
+  };
+
+  // The weights' scales of 64 stages, a lane each; 0 for stages past the last.
+  const int wb = min(n0 + wn * (FH * 16), p.n - 1) / kF8Block;
+  const size_t ws_row = ((size_t)expert * ((p.n + kF8Block - 1) / kF8Block) + wb) * blocks;
+  float ws[HALVES];
+  auto load_window = [&](int s) {
+#pragma unroll
+    for (int h = 0; h < HALVES; ++h) {
+      const float v = (h ? p.w1_scale : p.w0_scale)[ws_row + min(s + lane, blocks - 1)];
+      ws[h] = s + lane < blocks ? v : 0.0f;
+    }
+  };
+
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int a = 0; a < FM; ++a)
+#pragma unroll
+    for (int b = 0; b < FN; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const int a_row = wm * (BM / WM) + j, w_row = BM + wn * (BN / WN) + j;
+  const int col0 = place_of(j, g) * 16, col1 = place_of(j, g + 4) * 16;  // rows 16 apart have the same order of places
+  auto fragment = [&](const uint8_t* cur, int row) {
+    const uint8_t* at = cur + row * kF8Block;
+    const i32x4 c[2] = {*reinterpret_cast<const i32x4*>(at + col0), *reinterpret_cast<const i32x4*>(at + col1)};
+    return Fragment<EXACT>(c);
+  };
+  // One stage.  Before it is read, its loads have to have arrived (the stages after it stay in flight) and every
+  // wave has to have read the stage whose place the next load takes.
+  auto stage = [&](const uint8_t* cur, uint8_t* next, int s) {
+    wait_loads<(NST - 2) * (kLoads + 1)>();
+    wave_barrier();
+    issue(next, s + NST - 1);
+    float sw[HALVES];
+#pragma unroll
+    for (int h = 0; h < HALVES; ++h)
+      sw[h] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ws[h]), s & 63));
+    const float* scales = reinterpret_cast<const float*>(cur + kCodes);
+    Fragment<EXACT> fw[FN];
+#pragma unroll
+    for (int b = 0; b < FN; ++b) fw[b] = fragment(cur, w_row + 16 * b);
+#pragma unroll
+    for (int a = 0; a < FM; ++a) {
+      const Fragment<EXACT> fa = fragment(cur, a_row + 16 * a);
+      const float sa = scales[a_row + 16 * a];
+#pragma unroll
+      for (int b = 0; b < FN; ++b) {
+        const f32x4 sum = Fragment<EXACT>::multiply(fw[b], fa);
+        const float scale = sa * sw[b / FH];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[a][b][i] = fmaf(sum[i], scale, acc[a][b][i]);
+      }
+    }
+  };
+
+  load_window(0);
+  issue(c0, 0);
+  if (NST > 2) {
+    issue(c1, 1);
+    issue(c2, 2);
+  }
+  // Whole turns: the stages past the last one add zeros.
+  for (int s = 0; s < blocks; s += NST) {
+    if (s > 0 && (s & 63) == 0) load_window(s);
+    if (NST == 2) {
+      stage(c0, c1, s);
+      stage(c1, c0, s + 1);
+    } else {
+      stage(c0, c3, s);
+      stage(c1, c0, s + 1);
+      stage(c2, c1, s + 2);
+      stage(c3, c2, s + 3);
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(0);  // no load to LDS outlives the workgroup
+
+  // Lane j + 16 g of fragment (a, b): activation row 16 a + j, weight rows 4 g .. 4 g + 3 of b.
+  constexpr int kSpan = kPair ? 8 : 4;
+  auto result = [&](int a, int b, float (&v)[kSpan]) {
+#pragma unroll
+    for (int i = 0; i < kSpan; ++i) {
+      v[i] = acc[a][b + i / 4][i % 4];
+      if (HALVES == 2) v[i] = swiglu(v[i], acc[a][(HALVES - 1) * FH + b + i / 4][i % 4]);
+    }
+  };
+  const int col = n0 + wn * (FH * 16) + (kPair ? 8 * g : 4 * g);  // of fragment 0
+  if (HALVES == 2 && p.out_scale) {
+#pragma unroll
+    for (int a = 0; a < FM; ++a) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int b = 0; b < FH; b += kPair ? 2 : 1) {
+        float v[kSpan];
+        result(a, b, v);
+#pragma unroll
+        for (int i = 0; i < kSpan; ++i) {
+          acc[a][b + i / 4][i % 4] = v[i];
+          top = max(top, f8_bits(v[i]) & 0x7fffffffu);
+        }
+      }
+      top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+      if (g == 0) tops[a_row + 16 * a][wn] = top;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int a = 0; a < FM; ++a) {
+      const int r = tile_row(p, start, len, a_row + 16 * a);
+      if (r < 0) continue;
+      uint32_t top = 0;
+#pragma unroll
+      for (int w = 0; w < WN; ++w) top = max(top, tops[a_row + 16 * a][w]);
+      const F8Scale s(top, false);
+#pragma unroll
+      for (int b = 0; b < FH; b += kPair ? 2 : 1) {
+        float v[kSpan];
+#pragma unroll
+        for (int i = 0; i < kSpan; ++i) v[i] = acc[a][b + i / 4][i % 4];
+        uint32_t codes[kSpan / 4];
+        f8_codes(v, s, codes);
+        uint8_t* d = reinterpret_cast<uint8_t*>(p.out) + (size_t)r * p.n + col + 16 * b;
+        if (kPair) *reinterpret_cast<uint2*>(d) = make_uint2(codes[0], codes[kSpan / 4 - 1]);
+        else *reinterpret_cast<uint32_t*>(d) = codes[0];
+      }
+      if (wn == 0 && g == 0) p.out_scale[(size_t)r * (p.n / kF8Block) + rb] = s.scale;
+    }
+    return;
+  }
+  auto write = [&](auto store) {
+#pragma unroll
+    for (int a = 0; a < FM; ++a) {
+      const int r = tile_row(p, start, len, a_row + 16 * a);
+#pragma unroll
+      for (int b = 0; b < FH; b += kPair ? 2 : 1) {
+        float v[kSpan];
+        result(a, b, v);
+        if (r >= 0) store(r, col + 16 * b, v);
+      }
+    }
+  };
+  if (p.n % kSpan != 0)
+    write([&](int r, int c, const float (&v)[kSpan]) { store_odd<kSpan>(p, r, c, v); });
+  else if (p.out_bf16)
+    write([&](int r, int c, const float (&v)[kSpan]) { store_bf16<kSpan>(p, r, c, v); });
+  else
+    write([&](int r, int c, const float (&v)[kSpan]) { store_f32<kSpan>(p, r, c, v); });
+}
+
 // Tiles of at most bm rows there can be: an expert's last tile may be partly filled, at most one more per expert
 // that has pairs.  64 bits: m and n go up to 2^31 - 1.
 int64_t most_tiles(const F8MatmulParams& p, int bm) {
@@ -317,11 +592,48 @@ hipError_t launch_direct_pair(const F8MatmulParams& p, hipStream_t stream, bool 
   return hipGetLastError();
 }
 
+template <int BM, int BN, int WM, int WN, int NST, int HALVES, bool EXACT>
+hipError_t launch_tiled(const F8MatmulParams& p, hipStream_t stream, bool launch) {
+  const int64_t tiles = most_tiles(p, BM);
+  const int64_t row_blocks = ((int64_t)p.n + BN / HALVES - 1) / (BN / HALVES);
+  const int64_t grid = (tiles + kXcds - 1) / kXcds * kXcds * row_blocks;
+  if (grid * (WM * WN * 64) > kMostThreads) return hipErrorInvalidConfiguration;
+  if (!launch) return hipSuccess;
+  hipLaunchKernelGGL((tiled_kernel<BM, BN, WM, WN, NST, HALVES, EXACT>), dim3((unsigned)grid), dim3(WM * WN * 64), 0,
+                     stream, p, (int)tiles, (int)row_blocks);
+  return hipGetLastError();
+}
+
 // Without `launch` it says whether the launch could be made.
 hipError_t choose(const F8MatmulParams& p, hipStream_t stream, bool launch) {
-  if (p.w1) return p.m <= 64 ? launch_direct_pair<1, 2>(p, stream, launch) : launch_direct_pair<2, 1>(p, stream, launch);
+  const int fill = p.offsets ? (p.m + p.E - 1) / p.E : 0;  // pairs an expert gets on average
+  if (p.w1) {
+    if (p.m <= 64) return launch_direct_pair<1, 2>(p, stream, launch);
+    if (fill <= 28) return launch_tiled<32, 256, 1, 4, 2, 2, true>(p, stream, launch);
+    if (fill <= 160) return launch_tiled<128, 256, 2, 4, 2, 2, true>(p, stream, launch);
+    return launch_tiled<256, 256, 2, 4, 2, 2, true>(p, stream, launch);
+  }
+  if (p.offsets) {
+    if (p.m <= 16) return launch_direct<1, 8>(p, stream, launch);
+    if (fill <= 28) return launch_tiled<32, 128, 1, 4, 2, 1, true>(p, stream, launch);
+    if (fill <= 160)
+      return p.out_bf16 ? launch_tiled<128, 128, 2, 2, 2, 1, false>(p, stream, launch)
+                        : launch_tiled<128, 128, 2, 2, 2, 1, true>(p, stream, launch);
+    return p.out_bf16 ? launch_tiled<256, 256, 2, 4, 2, 1, false>(p, stream, launch)
+                      : launch_tiled<256, 256, 2, 4, 2, 1, true>(p, stream, launch);
+  }
   if (p.m <= 16) return launch_direct<1, 8>(p, stream, launch);
-  return launch_direct<2, 4>(p, stream, launch);
+  auto groups = [&](int64_t bm, int64_t bn) { return (p.m + bm - 1) / bm * ((p.n + bn - 1) / bn); };
+  if (groups(256, 256) >= 256)
+    return p.out_bf16 ? launch_tiled<256, 256, 2, 4, 2, 1, false>(p, stream, launch)
+                      : launch_tiled<256, 256, 2, 4, 2, 1, true>(p, stream, launch);
+  if (groups(128, 128) >= 200)
+    return p.out_bf16 ? launch_tiled<128, 128, 2, 2, 2, 1, false>(p, stream, launch)
+                      : launch_tiled<128, 128, 2, 2, 2, 1, true>(p, stream, launch);
+  if (groups(64, 128) >= 256) return launch_tiled<64, 128, 1, 4, 2, 1, true>(p, stream, launch);
+  if (groups(32, 128) > 256) return launch_tiled<32, 128, 1, 4, 2, 1, true>(p, stream, launch);
+  if (groups(32, 128) >= 128) return launch_tiled<32, 128, 1, 4, 4, 1, true>(p, stream, launch);
+  return launch_tiled<32, 64, 1, 2, 4, 1, true>(p, stream, launch);
 }
 
 }  // namespace
