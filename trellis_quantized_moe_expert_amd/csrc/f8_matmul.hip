@@ -443,31 +443,54 @@ __global__ __launch_bounds__(WM * WN * 64) void tiled_kernel(F8MatmulParams p, i
     const i32x4 c[2] = {*reinterpret_cast<const i32x4*>(at + col0), *reinterpret_cast<const i32x4*>(at + col1)};
     return Fragment<EXACT>(c);
   };
+  // The sums of a row of fragments join the running ones while the next row is multiplied, also from a stage to the next.
+  f32x4 old[FN];
+  float old_scale[HALVES];
+#pragma unroll
+  for (int b = 0; b < FN; ++b) old[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int h = 0; h < HALVES; ++h) old_scale[h] = 0.0f;
+  auto add_old = [&](int a, int b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[a][b][i] = fmaf(old[b][i], old_scale[b / FH], acc[a][b][i]);
+  };
   // One stage.  Before it is read, its loads have to have arrived (the stages after it stay in flight) and every
   // wave has to have read the stage whose place the next load takes.
   auto stage = [&](const uint8_t* cur, uint8_t* next, int s) {
     wait_loads<(NST - 2) * (kLoads + 1)>();
     wave_barrier();
+    const float* scales = reinterpret_cast<const float*>(cur + kCodes) + a_row;
+    Fragment<EXACT> fw[FN], fa = fragment(cur, a_row);
+#pragma unroll
+    for (int b = 0; b < FN; ++b) fw[b] = fragment(cur, w_row + 16 * b);
+    float sa = scales[0], sw[HALVES];
+    __builtin_amdgcn_sched_barrier(0);
     issue(next, s + NST - 1);
-    float sw[HALVES];
 #pragma unroll
     for (int h = 0; h < HALVES; ++h)
       sw[h] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ws[h]), s & 63));
-    const float* scales = reinterpret_cast<const float*>(cur + kCodes);
-    Fragment<EXACT> fw[FN];
 #pragma unroll
-    for (int b = 0; b < FN; ++b) fw[b] = fragment(cur, w_row + 16 * b);
+    for (int b = 0; b < FN; ++b) add_old(FM - 1, b);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int a = 0; a < FM; ++a) {
-      const Fragment<EXACT> fa = fragment(cur, a_row + 16 * a);
-      const float sa = scales[a_row + 16 * a];
+      const int next_row = 16 * (a + 1 < FM ? a + 1 : a);
+      const Fragment<EXACT> fa_next = fragment(cur, a_row + next_row);
+      const float sa_next = scales[next_row];
+      __builtin_amdgcn_sched_barrier(0);
+      f32x4 sum[FN];
 #pragma unroll
       for (int b = 0; b < FN; ++b) {
-        const f32x4 sum = Fragment<EXACT>::multiply(fw[b], fa);
-        const float scale = sa * sw[b / FH];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[a][b][i] = fmaf(sum[i], scale, acc[a][b][i]);
+        sum[b] = Fragment<EXACT>::multiply(fw[b], fa);
+        if (a > 0) add_old(a - 1, b);
+        __builtin_amdgcn_sched_barrier(0);
       }
+#pragma unroll
+      for (int b = 0; b < FN; ++b) old[b] = sum[b];
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h) old_scale[h] = sa * sw[h];
+      fa = fa_next;
+      sa = sa_next;
     }
   };
 
@@ -490,6 +513,8 @@ __global__ __launch_bounds__(WM * WN * 64) void tiled_kernel(F8MatmulParams p, i
       stage(c3, c2, s + 3);
     }
   }
+#pragma unroll
+  for (int b = 0; b < FN; ++b) add_old(FM - 1, b);
   __builtin_amdgcn_s_waitcnt(0);  // no load to LDS outlives the workgroup
 
   // Lane j + 16 g of fragment (a, b): activation row 16 a + j, weight rows 4 g .. 4 g + 3 of b.
