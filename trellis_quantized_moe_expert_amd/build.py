@@ -14,8 +14,8 @@ host pass, which prints that it does not know the feature and ignores it; that w
 harmless.  After compiling, the build scans the device assembly and fails if any packed FP32
 instruction appears, so the property is checked on every build, not assumed.
 
-Machine verifier: the sources but those of UNVERIFIED are compiled with `-mllvm -verify-machineinstrs`, so that wrong code of the compiler's
-own passes ends the build.  It is there because of a case: with a fragment loaded under a condition and used in a
+Machine verifier: the sources but those of UNVERIFIED are compiled with
+`-mllvm -verify-machineinstrs`, so that wrong code of the compiler's own passes ends the build.  It is there because of a case: with a fragment loaded under a condition and used in a
 loop, the pass that forms memory clauses lost track of the fragment's registers, and an address was written over
 them.  The verifier changes no code.
 """
@@ -36,6 +36,8 @@ BUILD_DIR = os.path.join(os.path.dirname(_HERE), "_build")
 ARCH = "gfx950"
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 VERIFY = ["-mllvm", "-verify-machineinstrs"]
+# the pass behind the case above left out where it has met
+SOURCE_FLAGS = {"csrc/f8_matmul.hip": ["-mllvm", "-amdgpu-max-memory-clause=1"]}
 UNVERIFIED = ["csrc/expert.hip", "csrc/expert_lut.hip"]  # clean when checked by hand; minutes on every build
 # packed FP32 arithmetic mnemonics (fma, add, mul on two fp32 lanes)
 PACKED_FP32 = re.compile(r"\bv_pk_(fma|add|mul)_f32\b")
@@ -50,7 +52,7 @@ def hipcc() -> str:
 
 def compile_command(src: str, obj: str) -> list:
     return [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall", *DEVICE_FLAGS,
-            *([] if src in UNVERIFIED else VERIFY), "-save-temps=obj", "-c", os.path.join(_HERE, src), "-o", obj]
+            *([] if src in UNVERIFIED else VERIFY), *SOURCE_FLAGS.get(src, []), "-save-temps=obj", "-c", os.path.join(_HERE, src), "-o", obj]
 
 
 def link_command(objs: list, output: str) -> list:

@@ -82,212 +82,56 @@ __device__ inline void load_scales(const float* row, int first, int blocks, floa
 }
 
 // ---- the direct kernel ----------------------------------------------------------------------
-// One workgroup: 16 weight rows by MB * 16 activation rows; its W waves split the inputs, run by run of U blocks, and
-// add their sums through LDS.  Operands go from memory to registers: with few activation rows a call is a
-// stream of weights, and the more of them are asked for at once the better.
+// One workgroup: 16 weight rows by up to 16 activation rows, dense; its W waves split the inputs, run by run of U blocks,
+// and add their sums through LDS.  Operands go from memory to registers: with few activation rows a call is a
+// stream of weights, and the more of them are asked for at once the better.  1 x 4096 x 4096, 16.8 MB of weights:
+// 6.1 us, of which about 2 are the launch; 1 x 8192 x 8192: 15.8, 4.2 TB/s.
 // TAIL: the rows do not end with a run.
-template <int MB, int W, bool TAIL>
+template <int W, bool TAIL>
 __global__ __launch_bounds__(W * 64) void direct_kernel(F8MatmulParams p) {
   constexpr int U = 4;
-  __shared__ f32x4 red[W][MB][64];
+  __shared__ f32x4 red[W][64];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int j = lane & 15, g = lane >> 4;
-  const int row_blocks = (p.n + 15) >> 4;
-  const int tile = (int)blockIdx.x / row_blocks;
-  const int n0 = ((int)blockIdx.x - tile * row_blocks) * 16;
-  int expert = 0, start = tile * MB * 16, len = min(MB * 16, p.m - start);
-  if (p.offsets && !find_tile(p.offsets, p.E, p.m, MB * 16, tile, expert, start, len)) return;
-
+  const int n0 = (int)blockIdx.x * 16;
   const int blocks = (p.k + kF8Block - 1) / kF8Block;
   int first = wv * U;
   int at = first * kF8Block + g * 16;  // this lane's first byte of the run
-  const uint8_t* wc = p.w0 + ((size_t)expert * p.n + min(n0 + j, p.n - 1)) * p.k;
-  const float* ws = p.w0_scale + ((size_t)expert * ((p.n + kF8Block - 1) / kF8Block) + n0 / kF8Block) * blocks;
+  const uint8_t* wc = p.w0 + (size_t)min(n0 + j, p.n - 1) * p.k;
+  const float* ws = p.w0_scale + (size_t)(n0 / kF8Block) * blocks;
+  const int arow = min(j, p.m - 1);  // rows past the last read it again; never stored
+  const uint8_t* ac = p.a + (size_t)arow * p.k;
+  const float* as = p.a_scale + (size_t)arow * blocks;
   i32x4 w[U][2] = {};
-  if (first < blocks) load_blocks<U, TAIL>(wc + at, p.k - at, w);  // before the activation rows are looked up
-
-  const uint8_t* ac[MB];
-  const float* as[MB];
-#pragma unroll
-  for (int b = 0; b < MB; ++b) {
-    const int r = tile_row(p, start, len, 16 * b + j);
-    const size_t arow = (size_t)(r < 0 ? 0 : r / p.a_div);  // rows past the tile read row 0; never stored
-    ac[b] = p.a + arow * p.k;
-    as[b] = p.a_scale + arow * blocks;
-  }
-  f32x4 acc[MB];
-#pragma unroll
-  for (int b = 0; b < MB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (first < blocks) load_blocks<U, TAIL>(wc + at, p.k - at, w);
+  f32x4 acc{0.f, 0.f, 0.f, 0.f};
   for (; first < blocks; first += W * U) {
-    i32x4 a[MB][U][2];
-    float sw[U], sa[MB][U];
+    i32x4 a[U][2];
+    float sw[U], sa[U];
     load_scales<U, TAIL>(ws, first, blocks, sw);
-#pragma unroll
-    for (int b = 0; b < MB; ++b) {
-      load_blocks<U, TAIL>(ac[b] + at, p.k - at, a[b]);
-      load_scales<U, TAIL>(as[b], first, blocks, sa[b]);
-    }
+    load_blocks<U, TAIL>(ac + at, p.k - at, a);
+    load_scales<U, TAIL>(as, first, blocks, sa);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const Wide ww(w[u]);
+      const f32x4 part = multiply_block(Wide(w[u]), Wide(a[u]));
+      const float s = sw[u] * sa[u];
 #pragma unroll
-      for (int b = 0; b < MB; ++b) {
-        const f32x4 part = multiply_block(ww, Wide(a[b][u]));
-        const float s = sw[u] * sa[b][u];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[b][i] = fmaf(part[i], s, acc[b][i]);
-      }
+      for (int i = 0; i < 4; ++i) acc[i] = fmaf(part[i], s, acc[i]);
     }
     at += W * U * kF8Block;
     if (first + W * U < blocks) load_blocks<U, TAIL>(wc + at, p.k - at, w);
   }
-#pragma unroll
-  for (int b = 0; b < MB; ++b) red[wv][b][lane] = acc[b];
+  red[wv][lane] = acc;
   __syncthreads();
-  for (int q = threadIdx.x; q < MB * 64; q += W * 64) {
-    const int b = q >> 6, ln = q & 63;
-    const int r = tile_row(p, start, len, 16 * b + (ln & 15));
-    if (r < 0) continue;
-    f32x4 y = red[0][b][ln];
+  if (wv != 0 || j >= p.m) return;
+  f32x4 y = red[0][lane];
 #pragma unroll
-    for (int u = 1; u < W; ++u) y += red[u][b][ln];
-    const float v[4] = {y[0], y[1], y[2], y[3]};
-    const int c = n0 + 4 * (ln >> 4);
-    if (p.n % 4 != 0) store_odd<4>(p, r, c, v);
-    else if (p.out_bf16) store_bf16<4>(p, r, c, v);
-    else store_f32<4>(p, r, c, v);
-  }
-}
-
-// ---- the direct kernel of two matrices -------------------------------------------------------
-// One workgroup: 128 rows of both matrices by MB * 16 activation rows, so that it holds whole blocks of its outputs and
-// can leave them in 8 bits.  Wave i takes 16 rows (i % 8) of both and part i / 8 of the inputs.
-template <int MB, int S>
-__global__ __launch_bounds__(S * 512) void direct_pair_kernel(F8MatmulParams p) {
-  constexpr int U = 2;
-  __shared__ f32x4 red[S][8][2 * MB][64];
-  __shared__ uint32_t tops[MB * 16][8];
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int j = lane & 15, g = lane >> 4;
-  const int part = wv >> 3, group = wv & 7;
-  const int row_blocks = p.n / kF8Block;  // an expert's rows are whole blocks
-  const int tile = (int)blockIdx.x / row_blocks, rb = (int)blockIdx.x - tile * row_blocks;
-  const int n0 = rb * kF8Block + group * 16;
-  int expert, start, len;
-  if (!find_tile(p.offsets, p.E, p.m, MB * 16, tile, expert, start, len)) return;
-
-  const int blocks = p.k / kF8Block;
-  int first = part * U;
-  int at = first * kF8Block + g * 16;
-  const size_t wrow = ((size_t)expert * p.n + n0 + j) * p.k;
-  const uint8_t* wc[2] = {p.w0 + wrow, p.w1 + wrow};
-  const size_t wsrow = ((size_t)expert * row_blocks + rb) * blocks;
-  const float* ws[2] = {p.w0_scale + wsrow, p.w1_scale + wsrow};
-  i32x4 w[2][U][2] = {};
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    if (first < blocks) load_blocks<U, true>(wc[h] + at, p.k - at, w[h]);
-
-  const uint8_t* ac[MB];
-  const float* as[MB];
-#pragma unroll
-  for (int b = 0; b < MB; ++b) {
-    const int r = tile_row(p, start, len, 16 * b + j);
-    const size_t arow = (size_t)(r < 0 ? 0 : r / p.a_div);  // rows past the tile read row 0; never stored
-    ac[b] = p.a + arow * p.k;
-    as[b] = p.a_scale + arow * blocks;
-  }
-  f32x4 acc[2][MB];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int b = 0; b < MB; ++b) acc[h][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (; first < blocks; first += S * U) {
-    i32x4 a[MB][U][2];
-    float sw[2][U], sa[MB][U];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) load_scales<U, true>(ws[h], first, blocks, sw[h]);
-#pragma unroll
-    for (int b = 0; b < MB; ++b) {
-      load_blocks<U, true>(ac[b] + at, p.k - at, a[b]);
-      load_scales<U, true>(as[b], first, blocks, sa[b]);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const Wide ww[2] = {Wide(w[0][u]), Wide(w[1][u])};
-#pragma unroll
-      for (int b = 0; b < MB; ++b) {
-        const Wide aa(a[b][u]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const f32x4 sum = multiply_block(ww[h], aa);
-          const float s = sw[h][u] * sa[b][u];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[h][b][i] = fmaf(sum[i], s, acc[h][b][i]);
-        }
-      }
-    }
-    at += S * U * kF8Block;
-    if (first + S * U < blocks) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) load_blocks<U, true>(wc[h] + at, p.k - at, w[h]);
-    }
-  }
-  if (part > 0) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int b = 0; b < MB; ++b) red[part][group][h * MB + b][lane] = acc[h][b];
-  }
-  __syncthreads();
-  if (part == 0) {
-#pragma unroll
-    for (int u = 1; u < S; ++u)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int b = 0; b < MB; ++b) acc[h][b] += red[u][group][h * MB + b][lane];
-  }
-  float v[MB][4];
-#pragma unroll
-  for (int b = 0; b < MB; ++b)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[b][i] = swiglu(acc[0][b][i], acc[1][b][i]);
-  if (p.out_scale) {
-    if (part == 0) {
-#pragma unroll
-      for (int b = 0; b < MB; ++b) {
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, f8_bits(v[b][i]) & 0x7fffffffu);
-        top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
-        top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-        if (g == 0) tops[16 * b + j][group] = top;
-      }
-    }
-    __syncthreads();
-  }
-  if (part != 0) return;
+  for (int u = 1; u < W; ++u) y += red[u][lane];
+  const float v[4] = {y[0], y[1], y[2], y[3]};
   const int c = n0 + 4 * g;
-#pragma unroll
-  for (int b = 0; b < MB; ++b) {
-    const int r = tile_row(p, start, len, 16 * b + j);
-    if (r < 0) continue;
-    if (p.out_scale) {
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = max(top, tops[16 * b + j][i]);
-      const F8Scale s(top, false);
-      uint32_t codes[1];
-      f8_codes(v[b], s, codes);
-      *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(p.out) + (size_t)r * p.n + c) = codes[0];
-      if (group == 0 && g == 0) p.out_scale[(size_t)r * row_blocks + rb] = s.scale;
-    } else if (p.out_bf16) {
-      store_bf16<4>(p, r, c, v[b]);
-    } else {
-      store_f32<4>(p, r, c, v[b]);
-    }
-  }
+  if (p.n % 4 != 0) store_odd<4>(p, j, c, v);
+  else if (p.out_bf16) store_bf16<4>(p, j, c, v);
+  else store_f32<4>(p, j, c, v);
 }
 
 // ---- the tiled kernel -----------------------------------------------------------------------
@@ -320,31 +164,51 @@ template <> struct Fragment<false> {
   }
 };
 
-template <int BM, int BN, int WM, int WN, int NST, int HALVES, bool EXACT>
-__global__ __launch_bounds__(WM * WN * 64) void tiled_kernel(F8MatmulParams p, int tiles, int row_blocks) {
-  constexpr int kThreads = WM * WN * 64;
+// The tile and row block of a workgroup of a dense product: each XCD gets a run of consecutive blocks, as many as any
+// other, walked down columns of 8 tiles (the last column may be narrower), so that the blocks running at a time
+// share few operand rows.
+__device__ inline bool dense_block(int tiles, int row_blocks, int b, int& tile, int& rb) {
+  const int total = tiles * row_blocks, each = (total + kXcds - 1) / kXcds;
+  const int at = b % kXcds * each + b / kXcds;
+  const int column = at / (8 * row_blocks), in = at % (8 * row_blocks);
+  const int width = min(8, tiles - column * 8);
+  if (b / kXcds >= each || at >= total) return false;
+  tile = column * 8 + in % width;
+  rb = in / width;
+  return true;
+}
+
+template <int BM, int BN, int WM, int WN, int NST, int HALVES, bool EXACT, int KG>
+__global__ __launch_bounds__(KG * WM * WN * 64) void tiled_kernel(F8MatmulParams p, int tiles, int row_blocks) {
+  constexpr int kThreads = WM * WN * 64;              // of a group
   constexpr int kRows = BM + BN;                      // rows of a stage: activations, then weights
   constexpr int kChunks = kF8Block / 16;              // of a row in a stage
-  constexpr int kLoads = kRows * kChunks / kThreads;  // 16-byte loads of a thread and stage
+  constexpr int kLoads = (kRows * kChunks + kThreads - 1) / kThreads;  // 16-byte loads of a thread and stage
   constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
   constexpr int FH = FN / HALVES;                     // fragments of one matrix
   constexpr bool kPair = FH % 2 == 0;                 // two fragments side by side: 8 outputs in a lane
-  static_assert(kRows * kChunks % kThreads == 0 && BM * kChunks % kThreads == 0, "a load is of one operand");
   static_assert(BM <= kThreads && FH >= 1 && FH * 16 <= kF8Block && (NST == 2 || NST == 4), "");
-  constexpr int kCodes = kRows * kF8Block, kStage = kCodes + kThreads * 4;
-  __shared__ __attribute__((aligned(1024))) uint8_t c0[kStage];
-  __shared__ __attribute__((aligned(1024))) uint8_t c1[kStage];
-  __shared__ __attribute__((aligned(1024))) uint8_t c2[NST > 2 ? kStage : 16];
-  __shared__ __attribute__((aligned(1024))) uint8_t c3[NST > 2 ? kStage : 16];
+  static_assert(KG == 1 || HALVES == 1, "groups are joined before the results are used");
+  constexpr int kCodes = kLoads * kThreads * 16, kStage = kCodes + kThreads * 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t c0[KG * kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t c1[KG * kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t c2[NST > 2 ? KG * kStage : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t c3[NST > 2 ? KG * kStage : 16];
   __shared__ uint32_t tops[HALVES == 2 ? BM : 1][WN];
 
-  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int kg = wave / (WM * WN), wv = wave % (WM * WN);  // group, wave in it
+  const int tid = wv * 64 + lane;
   const int wm = wv / WN, wn = wv % WN;
   const int j = lane & 15, g = lane >> 4;
 
   int tile, rb;
-  tile_of_block(p, tiles, row_blocks, (int)blockIdx.x, tile, rb);
-  if (tile >= tiles) return;
+  if (p.offsets) {
+    tile_of_block(p, tiles, row_blocks, (int)blockIdx.x, tile, rb);
+    if (tile >= tiles) return;
+  } else if (!dense_block(tiles, row_blocks, (int)blockIdx.x, tile, rb)) {
+    return;
+  }
   int expert = 0, start = tile * BM, len = min(BM, p.m - start);
   if (p.offsets && !find_tile(p.offsets, p.E, p.m, BM, tile, expert, start, len)) return;
   const int n0 = rb * (BN / HALVES);
@@ -370,10 +234,10 @@ __global__ __launch_bounds__(WM * WN * 64) void tiled_kernel(F8MatmulParams p, i
   // 2^30 bytes); their scales, a thirty-second of the codes, likewise.
   const int a_base = p.offsets ? 0 : start;
   const size_t w_base = ((size_t)expert * p.n + n0) * p.k;
-  const __amdgpu_buffer_rsrc_t ra = product_rsrc(p.a + (size_t)a_base * p.k);
+  const uint8_t* const a_codes = p.a + (size_t)a_base * p.k;
+  const uint8_t* const w0_codes = p.w0 + w_base;
+  const uint8_t* const w1_codes = HALVES == 2 ? p.w1 + w_base : nullptr;
   const __amdgpu_buffer_rsrc_t rs = product_rsrc(p.a_scale + (size_t)a_base * blocks);
-  const __amdgpu_buffer_rsrc_t rw0 = product_rsrc(p.w0 + w_base);
-  const __amdgpu_buffer_rsrc_t rw1 = product_rsrc(HALVES == 2 ? p.w1 + w_base : p.w0 + w_base);
 
   // Load i of a thread: LDS row and first byte in the row of the stage.
   auto load_at = [&](int i, int& r, int& byte) {
@@ -386,47 +250,53 @@ __global__ __launch_bounds__(WM * WN * 64) void tiled_kernel(F8MatmulParams p, i
   for (int i = 0; i < kLoads; ++i) {
     int r, byte;
     load_at(i, r, byte);
-    if (i * kThreads < BM * kChunks) {
+    if (r < BM) {
       const int row = act_row(r);
       off[i] = row < 0 ? kNoRow : (uint32_t)((size_t)(row - a_base) * p.k) + byte;
     } else {
       int half;
       const int row = weight_row(r - BM, half);
-      off[i] = row < p.n ? (uint32_t)((size_t)(row - n0) * p.k) + byte : kNoRow;
+      off[i] = r < kRows && row < p.n ? (uint32_t)((size_t)(row - n0) * p.k) + byte : kNoRow;
     }
   }
   const int scale_row = tid < BM ? act_row(tid) : -1;
   const uint32_t scale_off = scale_row < 0 ? kNoRow : (uint32_t)((size_t)(scale_row - a_base) * blocks * 4);
-  auto issue = [&](uint8_t* dst, int s) {
+  // Loads [i0, i1) of stage s's codes; its scales.
+  auto issue_codes = [&](uint8_t* dst, int s, int i0, int i1) __attribute__((always_inline)) {
+    const int block = s * KG + kg, so = min(block, blocks) * kF8Block;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
+      if (i < i0 || i >= i1) continue;
       // chunks past the row's end, and stages past the last
       int r, byte;
       load_at(i, r, byte);
-      const uint32_t o = s * kF8Block + byte < p.k ? off[i] : kNoRow;
-      const int so = min(s, blocks) * kF8Block;
-      lds_void* at = (lds_void*)(dst + (i * kThreads + wv * 64) * 16);
-      if (i * kThreads < BM * kChunks) {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, at, 16, o, so, 0, 0);
-      } else {
-        int half = 0;  // a wave's load is of rows of one fragment, so of one matrix
-        if (HALVES == 2) weight_row((i * kThreads + wv * 64) / kChunks - BM, half);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(half ? rw1 : rw0, at, 16, o, so, 0, 0);
-      }
+      const uint32_t o = block * kF8Block + byte < p.k ? off[i] : kNoRow;
+      lds_void* at = (lds_void*)(dst + kg * kStage + (i * kThreads + wv * 64) * 16);
+      const int row = (i * kThreads + wv * 64) / kChunks;  // a wave's load is of eight rows of one fragment
+      const bool of_a = (i + 1) * kThreads <= BM * kChunks || (i * kThreads < BM * kChunks && row < BM);
+      int half = 0;
+      if (HALVES == 2) weight_row(row - BM, half);
+      const uint8_t* base = of_a ? a_codes : HALVES == 2 && half ? w1_codes : w0_codes;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(product_rsrc(base), at, 16, o, so, 0, 0);
     }
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(dst + kCodes + wv * 256), 4, s < blocks ? scale_off : kNoRow,
-                                             min(s, blocks) * 4, 0, 0);
+  };
+  auto issue_scales = [&](uint8_t* dst, int s) __attribute__((always_inline)) {
+    const int block = s * KG + kg;
+    const uint32_t o = block < blocks ? scale_off : kNoRow;
+    lds_void* at = (lds_void*)(dst + kg * kStage + kCodes + wv * 256);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, at, 4, o, min(block, blocks) * 4, 0, 0);
   };
 
-  // The weights' scales of 64 stages, a lane each; 0 for stages past the last.
+  // The weights' scales of the group's 64 stages from s on, a lane each; 0 for stages past the last.
   const int wb = min(n0 + wn * (FH * 16), p.n - 1) / kF8Block;
   const size_t ws_row = ((size_t)expert * ((p.n + kF8Block - 1) / kF8Block) + wb) * blocks;
   float ws[HALVES];
-  auto load_window = [&](int s) {
+  auto load_window = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
     for (int h = 0; h < HALVES; ++h) {
-      const float v = (h ? p.w1_scale : p.w0_scale)[ws_row + min(s + lane, blocks - 1)];
-      ws[h] = s + lane < blocks ? v : 0.0f;
+      const int block = (s + lane) * KG + kg;
+      const float v = (h ? p.w1_scale : p.w0_scale)[ws_row + min(block, blocks - 1)];
+      ws[h] = block < blocks ? v : 0.0f;
     }
   };
 
@@ -438,10 +308,10 @@ __global__ __launch_bounds__(WM * WN * 64) void tiled_kernel(F8MatmulParams p, i
 
   const int a_row = wm * (BM / WM) + j, w_row = BM + wn * (BN / WN) + j;
   const int col0 = place_of(j, g) * 16, col1 = place_of(j, g + 4) * 16;  // rows 16 apart have the same order of places
-  auto fragment = [&](const uint8_t* cur, int row) {
+  struct Raw { i32x4 c[2]; };
+  auto read = [&](const uint8_t* cur, int row) __attribute__((always_inline)) {
     const uint8_t* at = cur + row * kF8Block;
-    const i32x4 c[2] = {*reinterpret_cast<const i32x4*>(at + col0), *reinterpret_cast<const i32x4*>(at + col1)};
-    return Fragment<EXACT>(c);
+    return Raw{{*reinterpret_cast<const i32x4*>(at + col0), *reinterpret_cast<const i32x4*>(at + col1)}};
   };
   // The sums of a row of fragments join the running ones while the next row is multiplied, also from a stage to the next.
   f32x4 old[FN];
@@ -450,76 +320,115 @@ __global__ __launch_bounds__(WM * WN * 64) void tiled_kernel(F8MatmulParams p, i
   for (int b = 0; b < FN; ++b) old[b] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int h = 0; h < HALVES; ++h) old_scale[h] = 0.0f;
-  auto add_old = [&](int a, int b) {
+  auto add_old = [&](int a, int b) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[a][b][i] = fmaf(old[b][i], old_scale[b / FH], acc[a][b][i]);
   };
   // One stage.  Before it is read, its loads have to have arrived (the stages after it stay in flight) and every
-  // wave has to have read the stage whose place the next load takes.
-  auto stage = [&](const uint8_t* cur, uint8_t* next, int s) {
+  // wave has to have read the stage whose place the next load takes.  A large tile's next loads go out one by one
+  // between the first half's products: all at once they hold up the wave, and the products behind them, until the address
+  // unit has taken them (4096 x 8192 x 8192: 241 us, at once 257).  A small one waits for memory and asks at once.
+  constexpr bool kEarly = BM <= 64;
+  // N: fragments of rows that are multiplied, the others hold no row.
+  auto stage = [&](auto fragments, const uint8_t* buf, uint8_t* next, int s) __attribute__((always_inline)) {
+    constexpr int N = decltype(fragments)::value;
+    constexpr int kIssue = N * FN > 1 ? N * FN / 2 : 1;
     wait_loads<(NST - 2) * (kLoads + 1)>();
     wave_barrier();
+    if (kEarly) issue_codes(next, s + NST - 1, 0, kLoads);
+    const uint8_t* cur = buf + kg * kStage;
     const float* scales = reinterpret_cast<const float*>(cur + kCodes) + a_row;
-    Fragment<EXACT> fw[FN], fa = fragment(cur, a_row);
-#pragma unroll
-    for (int b = 0; b < FN; ++b) fw[b] = fragment(cur, w_row + 16 * b);
+    Fragment<EXACT> fw[FN], fa(read(cur, a_row).c);
     float sa = scales[0], sw[HALVES];
-    __builtin_amdgcn_sched_barrier(0);
-    issue(next, s + NST - 1);
+    if (!EXACT) __builtin_amdgcn_sched_barrier(0);  // the products begin as the fragments come
+#pragma unroll
+    for (int b = 0; b < FN; ++b) {
+      fw[b] = Fragment<EXACT>(read(cur, w_row + 16 * b).c);
+      if (!EXACT) __builtin_amdgcn_sched_barrier(0);
+    }
+    issue_scales(next, s + NST - 1);
 #pragma unroll
     for (int h = 0; h < HALVES; ++h)
       sw[h] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ws[h]), s & 63));
 #pragma unroll
-    for (int b = 0; b < FN; ++b) add_old(FM - 1, b);
-    __builtin_amdgcn_sched_barrier(0);
+    for (int b = 0; b < FN; ++b) add_old(N - 1, b);
+    if (!EXACT) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int a = 0; a < FM; ++a) {
-      const int next_row = 16 * (a + 1 < FM ? a + 1 : a);
-      const Fragment<EXACT> fa_next = fragment(cur, a_row + next_row);
+    for (int a = 0; a < N; ++a) {
+      const int next_row = 16 * (a + 1 < N ? a + 1 : a);
+      const Raw a_next = read(cur, a_row + next_row);
       const float sa_next = scales[next_row];
-      __builtin_amdgcn_sched_barrier(0);
+      if (!EXACT) __builtin_amdgcn_sched_barrier(0);
       f32x4 sum[FN];
 #pragma unroll
       for (int b = 0; b < FN; ++b) {
         sum[b] = Fragment<EXACT>::multiply(fw[b], fa);
         if (a > 0) add_old(a - 1, b);
-        __builtin_amdgcn_sched_barrier(0);
+        const int step = a * FN + b;
+        if (!kEarly) issue_codes(next, s + NST - 1, step * kLoads / kIssue, (step + 1) * kLoads / kIssue);
+        if (!EXACT) __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int b = 0; b < FN; ++b) old[b] = sum[b];
 #pragma unroll
       for (int h = 0; h < HALVES; ++h) old_scale[h] = sa * sw[h];
-      fa = fa_next;
+      fa = Fragment<EXACT>(a_next.c);
       sa = sa_next;
+      if (EXACT) __builtin_amdgcn_sched_barrier(0);
     }
   };
 
   load_window(0);
-  issue(c0, 0);
-  if (NST > 2) {
-    issue(c1, 1);
-    issue(c2, 2);
+#pragma unroll
+  for (int s = 0; s < NST - 1; ++s) {
+    uint8_t* dst = s == 0 ? c0 : s == 1 ? c1 : c2;
+    issue_scales(dst, s);
+    issue_codes(dst, s, 0, kLoads);
   }
   // Whole turns: the stages past the last one add zeros.
-  for (int s = 0; s < blocks; s += NST) {
-    if (s > 0 && (s & 63) == 0) load_window(s);
-    if (NST == 2) {
-      stage(c0, c1, s);
-      stage(c1, c0, s + 1);
-    } else {
-      stage(c0, c3, s);
-      stage(c1, c0, s + 1);
-      stage(c2, c1, s + 2);
-      stage(c3, c2, s + 3);
+  const int stages = (blocks + KG - 1) / KG;
+  auto run = [&](auto fragments) __attribute__((always_inline)) {
+    for (int s = 0; s < stages; s += NST) {
+      if (s > 0 && (s & 63) == 0) load_window(s);
+      if (NST == 2) {
+        stage(fragments, c0, c1, s);
+        stage(fragments, c1, c0, s + 1);
+      } else {
+        stage(fragments, c0, c3, s);
+        stage(fragments, c1, c0, s + 1);
+        stage(fragments, c2, c1, s + 2);
+        stage(fragments, c3, c2, s + 3);
+      }
     }
-  }
 #pragma unroll
-  for (int b = 0; b < FN; ++b) add_old(FM - 1, b);
+    for (int b = 0; b < FN; ++b) add_old(decltype(fragments)::value - 1, b);
+  };
+  // A wave whose second half of rows is empty (an expert's last tile) leaves it out.
+  constexpr bool kHalf = FM == 2 || (FM > 2 && !EXACT);
+  if (kHalf && len <= wm * (BM / WM) + BM / WM / 2) run(Step<(FM + 1) / 2>());
+  else run(Step<FM>());
   __builtin_amdgcn_s_waitcnt(0);  // no load to LDS outlives the workgroup
+  if constexpr (KG > 1) {
+    static_assert(KG <= 2 && BM * BN * 4 <= KG * kStage, "the second group's sums go through the first stage's place");
+    f32x4* sums = reinterpret_cast<f32x4*>(c0) + tid;
+    __syncthreads();
+    if (kg == 1) {
+#pragma unroll
+      for (int a = 0; a < FM; ++a)
+#pragma unroll
+        for (int b = 0; b < FN; ++b) sums[(a * FN + b) * kThreads] = acc[a][b];
+    }
+    __syncthreads();
+    if (kg == 1) return;
+#pragma unroll
+    for (int a = 0; a < FM; ++a)
+#pragma unroll
+      for (int b = 0; b < FN; ++b) acc[a][b] += sums[(a * FN + b) * kThreads];
+  }
 
   // Lane j + 16 g of fragment (a, b): activation row 16 a + j, weight rows 4 g .. 4 g + 3 of b.
   constexpr int kSpan = kPair ? 8 : 4;
-  auto result = [&](int a, int b, float (&v)[kSpan]) {
+  auto result = [&](int a, int b, float (&v)[kSpan]) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < kSpan; ++i) {
       v[i] = acc[a][b + i / 4][i % 4];
@@ -569,7 +478,7 @@ __global__ __launch_bounds__(WM * WN * 64) void tiled_kernel(F8MatmulParams p, i
     }
     return;
   }
-  auto write = [&](auto store) {
+  auto write = [&](auto store) __attribute__((always_inline)) {
 #pragma unroll
     for (int a = 0; a < FM; ++a) {
       const int r = tile_row(p, start, len, a_row + 16 * a);
@@ -596,69 +505,79 @@ int64_t most_tiles(const F8MatmulParams& p, int bm) {
   return ((int64_t)p.m + bm - 1) / bm;
 }
 
-template <int MB, int W>
+template <int W>
 hipError_t launch_direct(const F8MatmulParams& p, hipStream_t stream, bool launch) {
-  const int64_t grid = most_tiles(p, MB * 16) * (((int64_t)p.n + 15) / 16);
+  const int64_t grid = ((int64_t)p.n + 15) / 16;
   if (grid * (W * 64) > kMostThreads) return hipErrorInvalidConfiguration;
   if (!launch) return hipSuccess;
   if (p.k % (4 * kF8Block) == 0)
-    hipLaunchKernelGGL((direct_kernel<MB, W, false>), dim3((unsigned)grid), dim3(W * 64), 0, stream, p);
+    hipLaunchKernelGGL((direct_kernel<W, false>), dim3((unsigned)grid), dim3(W * 64), 0, stream, p);
   else
-    hipLaunchKernelGGL((direct_kernel<MB, W, true>), dim3((unsigned)grid), dim3(W * 64), 0, stream, p);
+    hipLaunchKernelGGL((direct_kernel<W, true>), dim3((unsigned)grid), dim3(W * 64), 0, stream, p);
   return hipGetLastError();
 }
 
-template <int MB, int S>
-hipError_t launch_direct_pair(const F8MatmulParams& p, hipStream_t stream, bool launch) {
-  const int64_t grid = most_tiles(p, MB * 16) * (p.n / kF8Block);
-  if (grid * (S * 512) > kMostThreads) return hipErrorInvalidConfiguration;
-  if (!launch) return hipSuccess;
-  hipLaunchKernelGGL((direct_pair_kernel<MB, S>), dim3((unsigned)grid), dim3(S * 512), 0, stream, p);
-  return hipGetLastError();
-}
-
-template <int BM, int BN, int WM, int WN, int NST, int HALVES, bool EXACT>
+template <int BM, int BN, int WM, int WN, int NST, int HALVES, bool EXACT, int KG = 1>
 hipError_t launch_tiled(const F8MatmulParams& p, hipStream_t stream, bool launch) {
   const int64_t tiles = most_tiles(p, BM);
   const int64_t row_blocks = ((int64_t)p.n + BN / HALVES - 1) / (BN / HALVES);
-  const int64_t grid = (tiles + kXcds - 1) / kXcds * kXcds * row_blocks;
-  if (grid * (WM * WN * 64) > kMostThreads) return hipErrorInvalidConfiguration;
+  const int64_t grid = p.offsets ? (tiles + kXcds - 1) / kXcds * kXcds * row_blocks
+                                 : (tiles * row_blocks + kXcds - 1) / kXcds * kXcds;
+  constexpr int threads = KG * WM * WN * 64;
+  if (grid * threads > kMostThreads) return hipErrorInvalidConfiguration;
   if (!launch) return hipSuccess;
-  hipLaunchKernelGGL((tiled_kernel<BM, BN, WM, WN, NST, HALVES, EXACT>), dim3((unsigned)grid), dim3(WM * WN * 64), 0,
-                     stream, p, (int)tiles, (int)row_blocks);
+  hipLaunchKernelGGL((tiled_kernel<BM, BN, WM, WN, NST, HALVES, EXACT, KG>), dim3((unsigned)grid), dim3(threads), 0, stream,
+                     p, (int)tiles, (int)row_blocks);
   return hipGetLastError();
 }
 
-// Without `launch` it says whether the launch could be made.
-hipError_t choose(const F8MatmulParams& p, hipStream_t stream, bool launch) {
-  const int fill = p.offsets ? (p.m + p.E - 1) / p.E : 0;  // pairs an expert gets on average
-  if (p.w1) {
-    if (p.m <= 64) return launch_direct_pair<1, 2>(p, stream, launch);
-    if (fill <= 28) return launch_tiled<32, 256, 1, 4, 2, 2, true>(p, stream, launch);
-    if (fill <= 160) return launch_tiled<128, 256, 2, 4, 2, 2, true>(p, stream, launch);
-    return launch_tiled<256, 256, 2, 4, 2, 2, true>(p, stream, launch);
-  }
-  if (p.offsets) {
-    if (p.m <= 16) return launch_direct<1, 8>(p, stream, launch);
-    if (fill <= 28) return launch_tiled<32, 128, 1, 4, 2, 1, true>(p, stream, launch);
-    if (fill <= 160)
-      return p.out_bf16 ? launch_tiled<128, 128, 2, 2, 2, 1, false>(p, stream, launch)
-                        : launch_tiled<128, 128, 2, 2, 2, 1, true>(p, stream, launch);
-    return p.out_bf16 ? launch_tiled<256, 256, 2, 4, 2, 1, false>(p, stream, launch)
-                      : launch_tiled<256, 256, 2, 4, 2, 1, true>(p, stream, launch);
-  }
-  if (p.m <= 16) return launch_direct<1, 8>(p, stream, launch);
+// Which kernel and tile.  Large tiles read the operands less often, small ones make more workgroups; below about one
+// workgroup a CU a second group of waves that takes every other stage hides the waits instead.  bf16 results of tiles
+// that wait for the matrix instructions come from the 8-bit ones, all others from the exact ones (see the top).  Times in us at
+// m x n x k, or tokens of a 256-expert, top-6 layer of 4096 x 2048, each side of a border:
+//   direct up to 16 rows  1 x 4096 x 4096 direct 6.1, 16 x 64 tiles 13.0; 17 rows 10.0, 32 x 64 8.9
+//   256 x 256 from 256    2048 x 8192 x 2048 (256 tiles) 33.8, 128 x 128 46.4; 2048 x 4096 x 4096 (128) 48.8, 41.7
+//   128 x 128 from 400    1024 x 8192 x 2048 (512) 23.6, 64 x 128 28.1; 1024 x 4096 x 4096 (256) 30.1, 26.2
+//   64 x 128 from 160     1000 x 2056 x 4096 (272) 23.0, 32 x 128 25.8, two groups 34; two groups up to 256: 512 x 4096 x
+//                         4096 (256) 18.1, 32 x 128 20.3, one group 21.9; 683 x 2056 x 4064, exact, (187) 24.8, 32 x 128 29.3
+//   32 x 128 from 160     256 x 4096 x 4096 (256) 15.0, 32 x 64 16.4; 128 x 4096 x 4096 (128) 14.5, 9.7; up to 256 in two
+//                         groups: 256 x 8192 x 2048 (512) one group 11.7; 300 x 2056 x 4064 (170) two 19.8
+//   exact, large          4096 x 8192 x 8192 128 x 128 493, 64 x 128 570; the 8-bit instructions 240 (256 x 256)
+//   gate+up               24 pairs an expert 32 rows 776, 64 rows 889; 48 pairs 1130, 959; 96 pairs 64 rows 1582, 128 rows 1213
+//   down                  24 pairs 32 rows 458, 64 rows 461; 48 pairs 64 rows 490, 128 rows 514; 96 pairs 664, 574;
+//                         96 pairs 128 rows 574, 256 rows 609; 192 pairs 970, 717
+// The experts' points are of uniform routing; few or small experts make fewer workgroups than there are CUs, and the
+// rule does not ask.  Without `launch` it says whether the launch could be made.
+template <bool EXACT>
+hipError_t launch_dense(const F8MatmulParams& p, hipStream_t stream, bool launch) {
   auto groups = [&](int64_t bm, int64_t bn) { return (p.m + bm - 1) / bm * ((p.n + bn - 1) / bn); };
-  if (groups(256, 256) >= 256)
-    return p.out_bf16 ? launch_tiled<256, 256, 2, 4, 2, 1, false>(p, stream, launch)
-                      : launch_tiled<256, 256, 2, 4, 2, 1, true>(p, stream, launch);
-  if (groups(128, 128) >= 200)
-    return p.out_bf16 ? launch_tiled<128, 128, 2, 2, 2, 1, false>(p, stream, launch)
-                      : launch_tiled<128, 128, 2, 2, 2, 1, true>(p, stream, launch);
-  if (groups(64, 128) >= 256) return launch_tiled<64, 128, 1, 4, 2, 1, true>(p, stream, launch);
-  if (groups(32, 128) > 256) return launch_tiled<32, 128, 1, 4, 2, 1, true>(p, stream, launch);
-  if (groups(32, 128) >= 128) return launch_tiled<32, 128, 1, 4, 4, 1, true>(p, stream, launch);
-  return launch_tiled<32, 64, 1, 2, 4, 1, true>(p, stream, launch);
+  if constexpr (!EXACT) {
+    if (groups(256, 256) >= 256) return launch_tiled<256, 256, 2, 4, 2, 1, false>(p, stream, launch);
+  }
+  if (groups(128, 128) >= 400) return launch_tiled<128, 128, 2, 2, 2, 1, EXACT>(p, stream, launch);
+  if (groups(64, 128) > 256) return launch_tiled<64, 128, 1, 4, 2, 1, EXACT>(p, stream, launch);
+  if (groups(64, 128) >= 160) return launch_tiled<64, 128, 2, 2, 2, 1, EXACT, 2>(p, stream, launch);
+  if (groups(32, 128) > 256) return launch_tiled<32, 128, 1, 4, 2, 1, EXACT>(p, stream, launch);
+  if (groups(32, 128) >= 160) return launch_tiled<32, 128, 1, 4, 2, 1, EXACT, 2>(p, stream, launch);
+  return launch_tiled<32, 64, 1, 2, 4, 1, EXACT, 2>(p, stream, launch);
+}
+
+hipError_t choose(const F8MatmulParams& p, hipStream_t stream, bool launch) {
+  if (!p.offsets) {
+    if (p.m <= 16) return launch_direct<8>(p, stream, launch);
+    return p.out_bf16 ? launch_dense<false>(p, stream, launch) : launch_dense<true>(p, stream, launch);
+  }
+  const int fill = (p.m + p.E - 1) / p.E;  // pairs an expert gets on average
+  if (p.w1) {
+    if (fill <= 28) return launch_tiled<32, 256, 1, 4, 2, 2, true>(p, stream, launch);
+    if (fill <= 64) return launch_tiled<64, 256, 1, 4, 2, 2, true>(p, stream, launch);
+    return launch_tiled<128, 256, 2, 4, 2, 2, true>(p, stream, launch);
+  }
+  if (fill <= 28) return launch_tiled<32, 128, 1, 4, 2, 1, true>(p, stream, launch);
+  if (fill <= 64) return launch_tiled<64, 128, 1, 4, 2, 1, true>(p, stream, launch);
+  if (!p.out_bf16) return launch_tiled<128, 128, 2, 2, 2, 1, true>(p, stream, launch);
+  if (fill <= 160) return launch_tiled<128, 128, 2, 2, 2, 1, false>(p, stream, launch);
+  return launch_tiled<256, 256, 2, 4, 2, 1, false>(p, stream, launch);
 }
 
 }  // namespace
