@@ -233,7 +233,7 @@ def test_product_matches_float64(m, n, k, kind):
 # every tile of the dense product: rows and columns past the tiles' ends, last blocks not full
 TILES = [(20, 8200, 96), (130, 4100, 1120), (280, 2056, 96), (290, 2050, 4160), (260, 4104, 2080), (300, 3300, 160),
          (1000, 2056, 160), (1001, 2063, 288), (1030, 3200, 96), (1100, 3207, 544), (4000, 4100, 64),
-         (3850, 4351, 352)]
+         (3850, 4351, 352), (683, 2056, 4064), (700, 1800, 608)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp32"])

@@ -544,6 +544,7 @@ hipError_t launch_tiled(const F8MatmulParams& p, hipStream_t stream, bool launch
 //                         groups: 256 x 8192 x 2048 (512) one group 11.7; 300 x 2056 x 4064 (170) two 19.8
 //   exact, large          4096 x 8192 x 8192 128 x 128 493, 64 x 128 570; the 8-bit instructions 240 (256 x 256)
 //   gate+up               24 pairs an expert 32 rows 776, 64 rows 889; 48 pairs 1130, 959; 96 pairs 64 rows 1582, 128 rows 1213
+//                         up to 128 workgroups four stages: 6 pairs (96) 29.8, two 38.2; 24 pairs (384) 78, 73
 //   down                  24 pairs 32 rows 458, 64 rows 461; 48 pairs 64 rows 490, 128 rows 514; 96 pairs 664, 574;
 //                         96 pairs 128 rows 574, 256 rows 609; 192 pairs 970, 717
 // The experts' points are of uniform routing; few or small experts make fewer workgroups than there are CUs, and the
@@ -569,6 +570,7 @@ hipError_t choose(const F8MatmulParams& p, hipStream_t stream, bool launch) {
   }
   const int fill = (p.m + p.E - 1) / p.E;  // pairs an expert gets on average
   if (p.w1) {
+    if ((int64_t)p.m * (p.n / kF8Block) <= 128) return launch_tiled<32, 256, 1, 4, 4, 2, true>(p, stream, launch);
     if (fill <= 28) return launch_tiled<32, 256, 1, 4, 2, 2, true>(p, stream, launch);
     if (fill <= 64) return launch_tiled<64, 256, 1, 4, 2, 2, true>(p, stream, launch);
     return launch_tiled<128, 256, 2, 4, 2, 2, true>(p, stream, launch);
