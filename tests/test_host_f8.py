@@ -144,6 +144,26 @@ def test_rows_and_strides_of_other_tensors_are_refused(gpu_arrays):  # noqa: F81
             x, kind, 5, 130, 160, residual, 140, residual_out, weight, q.QTIP_F8_F32, 1e-6, q.QTIP_F8_SCALE_AMAX, **a),
             good, bad, calls)
         calls.clear()
+    # whole arrays: the same checks, residual and values present or not
+    good = dict(x=array(5, 130, dtype="bfloat16"), residual=array(5, 130, dtype="bfloat16"),
+                residual_out=array(5, 130, dtype="bfloat16"), weight=array(130, dtype="bfloat16"), codes=array(5, 144),
+                scales=array(5, 2, dtype="float32"), values=array(5, 130, dtype="bfloat16"))
+    bad = [(key, lambda t=t: t.reshape(-1)[:-1].contiguous()) for key, t in good.items()]
+    bad += [(key, lambda t=t: array(*t.shape, dtype=str(t.dtype)[6:], device=1)) for key, t in good.items()]
+    bad += [(key, lambda t=t: t.half()) for key, t in good.items()]
+    norm = lambda x, weight, codes, scales, residual=None, residual_out=None, values=None: q.qtip_f8_rms_norm(
+        x, q.QTIP_F8_BF16, 5, 130, 130, residual, 130 if residual is not None else 0, residual_out, weight, q.QTIP_F8_BF16,
+        1e-6, q.QTIP_F8_SCALE_AMAX, codes, scales, values)
+    refusals(norm, good, bad, calls)
+    for left_out in ("values", "residual", "values residual"):
+        calls.clear()
+        drop = left_out.replace("residual", "residual residual_out").split()
+        some = {key: t for key, t in good.items() if key not in drop}
+        refusals(norm, some, [b for b in bad if b[0] in some], calls)
+        args = calls[0][1]
+        assert [args[i] for i in (0, 8, 12, 13)] == [good[k].data_ptr() for k in ("x", "weight", "codes", "scales")]
+        assert (args[5] is None) == ("residual" in left_out) and (args[14] is None) == ("values" in left_out)
+    calls.clear()
     f8 = getattr(torch, "float8_e4m3fn")
     q.qtip_f8_quantize(256, q.QTIP_F8_F32, 4, 128, 128, 1, 0, array(4, 128).view(f8), 256)   # codes as their values' type
     assert len(calls) == 1

@@ -696,9 +696,14 @@ def _f8_sizes(rows: int, cols: int, block_rows: int = 1) -> tuple:
 
 def qtip_f8_quantize(src, src_type, rows, cols, row_stride, block_rows, scale_rule, codes, scales, stream=None) -> None:
     fn = "qtip_f8_quantize"
-    _check_rows(fn, "src", _SRC_KINDS.get(src_type, (".", 0))[0], src, rows, cols, row_stride)
-    p = _pointers(fn, "ef", ("codes", "scales"), (codes, scales), _f8_sizes(rows, cols, max(block_rows, 1)))
-    _check(fn, lib().qtip_f8_quantize(_ptr(src), src_type, rows, cols, row_stride, block_rows, scale_rule, p[0], p[1],
+    kind, size = _SRC_KINDS.get(src_type, (".", 0))
+    sizes = _f8_sizes(rows, cols, max(block_rows, 1))
+    if row_stride == cols:
+        p = _pointers(fn, kind + "ef", ("src", "codes", "scales"), (src, codes, scales), (rows * cols * size, *sizes))
+    else:
+        _check_rows(fn, "src", kind, src, rows, cols, row_stride)
+        p = [_ptr(src)] + _pointers(fn, "ef", ("codes", "scales"), (codes, scales), sizes)
+    _check(fn, lib().qtip_f8_quantize(p[0], src_type, rows, cols, row_stride, block_rows, scale_rule, p[1], p[2],
                                       _stream(stream)))
 
 
@@ -707,20 +712,27 @@ def qtip_f8_rms_norm(x, type_, rows, cols, x_stride, residual, residual_stride, 
     fn = "qtip_f8_rms_norm"
     kind, size = _SRC_KINDS.get(type_, (".", 0))
     w_kind, w_size = _SRC_KINDS.get(weight_type, (".", 0))
-    _check_rows(fn, "x", kind, x, rows, cols, x_stride)
-    if residual is not None or residual_out is not None:
-        _check_rows(fn, "residual", kind, residual, rows, cols, residual_stride)
-        _check_rows(fn, "residual_out", kind, residual_out, rows, cols, residual_stride)
-    sizes = w_size * cols, *_f8_sizes(rows, cols), size * rows * cols
-    if values is None:
-        p = _pointers(fn, w_kind + "ef", ("weight", "codes", "scales"), (weight, codes, scales), sizes[:3])
-        p.append(None)
+    whole = size * rows * cols
+    summed = residual is not None or residual_out is not None
+    names, kinds, objs, sizes = ("weight", "codes", "scales"), w_kind + "ef", (weight, codes, scales), (
+        w_size * cols, *_f8_sizes(rows, cols))
+    if values is not None:
+        names, kinds, objs, sizes = (*names, "values"), kinds + kind, (*objs, values), (*sizes, whole)
+    if x_stride == cols and (not summed or residual_stride == cols):  # whole arrays all of them
+        if summed:
+            names, kinds, objs = ("x", "residual", "residual_out", *names), kind * 3 + kinds, (x, residual, residual_out, *objs)
+            p = _pointers(fn, kinds, names, objs, (whole, whole, whole, *sizes))
+        else:
+            p = _pointers(fn, kind + kinds, ("x", *names), (x, *objs), (whole, *sizes))
+            p[1:1] = None, None
     else:
-        p = _pointers(fn, w_kind + "ef" + kind, ("weight", "codes", "scales", "values"), (weight, codes, scales, values),
-                      sizes)
-    _check(fn, lib().qtip_f8_rms_norm(_ptr(x), type_, rows, cols, x_stride, _ptr(residual), residual_stride,
-                                      _ptr(residual_out), p[0], weight_type, eps, scale_rule, p[1], p[2], p[3],
-                                      _stream(stream)))
+        _check_rows(fn, "x", kind, x, rows, cols, x_stride)
+        if summed:
+            _check_rows(fn, "residual", kind, residual, rows, cols, residual_stride)
+            _check_rows(fn, "residual_out", kind, residual_out, rows, cols, residual_stride)
+        p = [_ptr(x), _ptr(residual), _ptr(residual_out)] + _pointers(fn, kinds, names, objs, sizes)
+    _check(fn, lib().qtip_f8_rms_norm(p[0], type_, rows, cols, x_stride, p[1], residual_stride, p[2], p[3], weight_type,
+                                      eps, scale_rule, p[4], p[5], p[6] if values is not None else None, _stream(stream)))
 
 
 def qtip_f8_matmul(a_codes, a_scales, m, w_codes, w_scales, n, k, out, out_dtype, stream=None) -> None:

@@ -187,13 +187,14 @@ __global__ __launch_bounds__(KG * WM * WN * 64) void tiled_kernel(F8MatmulParams
   constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
   constexpr int FH = FN / HALVES;                     // fragments of one matrix
   constexpr bool kPair = FH % 2 == 0;                 // two fragments side by side: 8 outputs in a lane
-  static_assert(BM <= kThreads && FH >= 1 && FH * 16 <= kF8Block && (NST == 2 || NST == 4), "");
+  static_assert(BM <= kThreads && FH >= 1 && FH * 16 <= kF8Block && NST >= 2 && NST <= 4, "");
   static_assert(KG == 1 || HALVES == 1, "groups are joined before the results are used");
+  constexpr int kWindow = 64 / NST * NST;             // stages whose weight scales a register holds, in whole turns
   constexpr int kCodes = kLoads * kThreads * 16, kStage = kCodes + kThreads * 4;
   __shared__ __attribute__((aligned(1024))) uint8_t c0[KG * kStage];
   __shared__ __attribute__((aligned(1024))) uint8_t c1[KG * kStage];
   __shared__ __attribute__((aligned(1024))) uint8_t c2[NST > 2 ? KG * kStage : 16];
-  __shared__ __attribute__((aligned(1024))) uint8_t c3[NST > 2 ? KG * kStage : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t c3[NST > 3 ? KG * kStage : 16];
   __shared__ uint32_t tops[HALVES == 2 ? BM : 1][WN];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -287,7 +288,7 @@ __global__ __launch_bounds__(KG * WM * WN * 64) void tiled_kernel(F8MatmulParams
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, at, 4, o, min(block, blocks) * 4, 0, 0);
   };
 
-  // The weights' scales of the group's 64 stages from s on, a lane each; 0 for stages past the last.
+  // The weights' scales of the group's stages from s on, a lane each; 0 for stages past the last.
   const int wb = min(n0 + wn * (FH * 16), p.n - 1) / kF8Block;
   const size_t ws_row = ((size_t)expert * ((p.n + kF8Block - 1) / kF8Block) + wb) * blocks;
   float ws[HALVES];
@@ -349,7 +350,7 @@ __global__ __launch_bounds__(KG * WM * WN * 64) void tiled_kernel(F8MatmulParams
     issue_scales(next, s + NST - 1);
 #pragma unroll
     for (int h = 0; h < HALVES; ++h)
-      sw[h] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ws[h]), s & 63));
+      sw[h] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ws[h]), s % kWindow));
 #pragma unroll
     for (int b = 0; b < FN; ++b) add_old(N - 1, b);
     if (!EXACT) __builtin_amdgcn_sched_barrier(0);
@@ -389,10 +390,14 @@ __global__ __launch_bounds__(KG * WM * WN * 64) void tiled_kernel(F8MatmulParams
   const int stages = (blocks + KG - 1) / KG;
   auto run = [&](auto fragments) __attribute__((always_inline)) {
     for (int s = 0; s < stages; s += NST) {
-      if (s > 0 && (s & 63) == 0) load_window(s);
+      if (s > 0 && s % kWindow == 0) load_window(s);
       if (NST == 2) {
         stage(fragments, c0, c1, s);
         stage(fragments, c1, c0, s + 1);
+      } else if (NST == 3) {
+        stage(fragments, c0, c2, s);
+        stage(fragments, c1, c0, s + 1);
+        stage(fragments, c2, c1, s + 2);
       } else {
         stage(fragments, c0, c3, s);
         stage(fragments, c1, c0, s + 1);
@@ -539,9 +544,10 @@ hipError_t launch_tiled(const F8MatmulParams& p, hipStream_t stream, bool launch
 //   256 x 256 from 256    2048 x 8192 x 2048 (256 tiles) 33.8, 128 x 128 46.4; 2048 x 4096 x 4096 (128) 48.8, 41.7
 //   128 x 128 from 400    1024 x 8192 x 2048 (512) 23.6, 64 x 128 28.1; 1024 x 4096 x 4096 (256) 30.1, 26.2
 //   64 x 128 from 160     1000 x 2056 x 4096 (272) 23.0, 32 x 128 25.8, two groups 34; two groups up to 256: 512 x 4096 x
-//                         4096 (256) 18.1, 32 x 128 20.3, one group 21.9; 683 x 2056 x 4064, exact, (187) 24.8, 32 x 128 29.3
-//   32 x 128 from 160     256 x 4096 x 4096 (256) 15.0, 32 x 64 16.4; 128 x 4096 x 4096 (128) 14.5, 9.7; up to 256 in two
-//                         groups: 256 x 8192 x 2048 (512) one group 11.7; 300 x 2056 x 4064 (170) two 19.8
+//                         4096 (256) 16.1, 32 x 128 20.3, one group 21.4; 683 x 2056 x 4064, exact, (187) 24.4, 32 x 128 29.3
+//   32 x 128 from 160     256 x 4096 x 4096 (256) 12.1, 32 x 64 16.4; 128 x 4096 x 4096 (128) 14.5, 9.7; two groups up to
+//                         256: 300 x 2056 x 4064 (170) 16.6, one 19.0
+//   stages of two groups  512 x 4096 x 4096 three 16.1, two 17.7; exact 683 x 2056 x 4064 three 28, two 24.4
 //   exact, large          4096 x 8192 x 8192 128 x 128 493, 64 x 128 570; the 8-bit instructions 240 (256 x 256)
 //   gate+up               24 pairs an expert 32 rows 776, 64 rows 889; 48 pairs 1130, 959; 96 pairs 64 rows 1582, 128 rows 1213
 //                         up to 128 workgroups four stages: 6 pairs (96) 29.8, two 38.2; 24 pairs (384) 78, 73
@@ -551,15 +557,16 @@ hipError_t launch_tiled(const F8MatmulParams& p, hipStream_t stream, bool launch
 // rule does not ask.  Without `launch` it says whether the launch could be made.
 template <bool EXACT>
 hipError_t launch_dense(const F8MatmulParams& p, hipStream_t stream, bool launch) {
+  constexpr int kDeep = EXACT ? 2 : 3;  // stages of two groups of waves, one workgroup a CU
   auto groups = [&](int64_t bm, int64_t bn) { return (p.m + bm - 1) / bm * ((p.n + bn - 1) / bn); };
   if constexpr (!EXACT) {
     if (groups(256, 256) >= 256) return launch_tiled<256, 256, 2, 4, 2, 1, false>(p, stream, launch);
   }
   if (groups(128, 128) >= 400) return launch_tiled<128, 128, 2, 2, 2, 1, EXACT>(p, stream, launch);
   if (groups(64, 128) > 256) return launch_tiled<64, 128, 1, 4, 2, 1, EXACT>(p, stream, launch);
-  if (groups(64, 128) >= 160) return launch_tiled<64, 128, 2, 2, 2, 1, EXACT, 2>(p, stream, launch);
+  if (groups(64, 128) >= 160) return launch_tiled<64, 128, 2, 2, kDeep, 1, EXACT, 2>(p, stream, launch);
   if (groups(32, 128) > 256) return launch_tiled<32, 128, 1, 4, 2, 1, EXACT>(p, stream, launch);
-  if (groups(32, 128) >= 160) return launch_tiled<32, 128, 1, 4, 2, 1, EXACT, 2>(p, stream, launch);
+  if (groups(32, 128) >= 160) return launch_tiled<32, 128, 1, 4, kDeep, 1, EXACT, 2>(p, stream, launch);
   return launch_tiled<32, 64, 1, 2, 4, 1, EXACT, 2>(p, stream, launch);
 }
 
