@@ -47,6 +47,20 @@ def test_quantise_next_to_the_borders(rule):
     same(quantise(x, "fp32", rule), f8.quantise(x.cpu().double().numpy(), rule))
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_sources_at_any_elements_address(kind):
+    import torch
+    say(f"quantise and norm from odd addresses {kind}")
+    g = torch.Generator().manual_seed(11)
+    flat = torch.randn(3000, generator=g).to(dtype_of(kind)).cuda()
+    for at in (1, 3, 5):
+        x = flat[at:at + 5 * 301].as_strided((5, 270), (301, 1), at)
+        same(quantise(x, kind, "amax"), f8.quantise(x.cpu().double().numpy(), "amax"))
+        w = flat[at + 1600:at + 1600 + 270]
+        res = flat[at + 1:].as_strided((5, 270), (280, 1), at + 1)
+        check_norm(x, kind, res, w, kind, 1e-6)
+
+
 @pytest.mark.parametrize("block_rows", [1, 128])
 @pytest.mark.parametrize("rule", ["amax", "pow2"])
 @pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
@@ -219,7 +233,8 @@ def check_product(a, w, kind):
 SIZES = [(1, 1, 16), (1, 16, 128), (1, 4096, 512), (2, 17, 144), (3, 100, 560), (15, 33, 1040), (16, 16, 2048),
          (17, 64, 512), (33, 48, 4096), (64, 130, 640), (65, 128, 128), (100, 257, 416), (128, 256, 256),
          (129, 72, 992), (255, 300, 1024), (256, 256, 4096), (300, 513, 160), (513, 1040, 2080), (1, 24, 8192),
-         (40, 50, 96), (20, 70, 32), (700, 300, 128), (520, 264, 1184), (4, 136, 4112), (1, 130, 16400)]
+         (40, 50, 96), (20, 70, 32), (700, 300, 128), (520, 264, 1184), (4, 136, 4112), (1, 130, 16400),
+         (40, 100, 20000), (300, 300, 9008), (330, 2100, 8720)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp32"])
@@ -233,7 +248,7 @@ def test_product_matches_float64(m, n, k, kind):
 # every tile of the dense product: rows and columns past the tiles' ends, last blocks not full
 TILES = [(20, 8200, 96), (130, 4100, 1120), (280, 2056, 96), (290, 2050, 4160), (260, 4104, 2080), (300, 3300, 160),
          (1000, 2056, 160), (1001, 2063, 288), (1030, 3200, 96), (1100, 3207, 544), (4000, 4100, 64),
-         (3850, 4351, 352), (683, 2056, 4064), (700, 1800, 608)]
+         (3850, 4351, 352), (683, 2056, 4064), (700, 1800, 608), (700, 1800, 16656)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp32"])
@@ -381,6 +396,10 @@ EXPERTS = [
     (600, 3, 2, 512, 256, True, 0.0),
     (260, 2, 2, 2048, 128, False, 0.0),
     (1500, 4, 1, 256, 512, True, 0.05),
+    (40, 16, 3, 8448, 128, False, 0.0),
+    (180, 8, 2, 8320, 128, False, 0.0),
+    (300, 4, 2, 8448, 256, False, 0.0),
+    (500, 2, 1, 128, 8448, False, 0.0),
 ]
 
 

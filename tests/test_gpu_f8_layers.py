@@ -285,8 +285,9 @@ def test_dense_chain_quantise_then_product():
 
 
 @pytest.mark.parametrize("m,n,k,kind", [(600_000, 16, 4096, "bf16"), (3, 600_000, 4096, "fp32"), (40, 1_100_000, 2048, "bf16"),
-                                        (1_100_000, 130, 2048, "fp32")])
-def test_products_of_matrices_past_2_31_bytes(m, n, k, kind):
+                                        (1_100_000, 130, 2048, "fp32"), (4200, 4112, 8336, "bf16"),
+                                        (4200, 4112, 8336, "fp32")])
+def test_products_of_large_matrices(m, n, k, kind):
     # rows repeat with a period, so that few of them have to be computed in float64; the last ones are looked at
     import torch
     say(f"e4m3 product {m}x{n}x{k}")
