@@ -458,3 +458,20 @@ def test_results_do_not_depend_on_the_run():
     for part in ("gate_up", "down"):
         assert np.array_equal(ex.run(part, "fp32"), ex.run(part, "fp32"))
     ex.close()
+
+
+def test_norm_of_a_very_long_row_of_equal_values():
+    import torch
+    say("norm of 2^28 equal values")
+    cols, value = 2 ** 28 + 40, float(np.float32(1.1))
+    x = torch.full((1, cols), value, device="cuda:0")
+    w = torch.ones(cols, device="cuda:0")
+    codes = torch.empty(1, -(-cols // 16) * 16, dtype=torch.uint8, device="cuda:0")
+    scales = torch.empty(1, -(-cols // 128), device="cuda:0")
+    vals = torch.empty_like(x)
+    q.qtip_f8_rms_norm(x, TYPE["fp32"], 1, cols, cols, None, 0, None, w, TYPE["fp32"], 1e-6, RULE["amax"], codes, scales, vals)
+    y = value / np.sqrt(value * value + 1e-6)
+    # eight squares in fp32, the eights in fp64, then as norm_bound: 6 + 16 sums of lanes and waves
+    lim = norm_bound(1024 * 8) * y
+    assert bool(((vals.double() - y).abs() <= lim).all())
+    assert bool((codes[0, :cols] == 0x7e).all()) and not bool(codes[0, cols:].any())

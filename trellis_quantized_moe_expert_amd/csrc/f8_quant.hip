@@ -3,8 +3,9 @@
 //
 //   norm: h = x, or x + residual rounded to the type;  y_c = h_c w_c / sqrt(sum h^2 / cols + eps)
 //
-// All are one pass over memory, bound by it: 8192 x 8192 bf16 in 1 x 128 blocks 43 us, 4.7 TB/s.  A thread takes eight neighbouring values (16 or 32 bytes, the widest loads), so a
-// block of 128 lies in 16 neighbouring lanes and its largest value is four lane moves away, without LDS.
+// All are one pass over memory, bound by it: 8192 x 8192 bf16 in 1 x 128 blocks 43 us, 4.7 TB/s.  A thread takes
+// eight neighbouring values (16 or 32 bytes, the widest loads), so a block of 128 lies in 16 neighbouring lanes and
+// its largest value is four lane moves away, without LDS.
 #include "f8_device.h"
 #include "f8_internal.h"
 
@@ -73,7 +74,8 @@ __device__ inline uint32_t top_of(const float (&v)[kPerThread]) {
 }
 
 // Codes of eight values from column c on; a row's bytes end with zeros at a multiple of 16.
-__device__ inline void store_codes(uint8_t* row, int64_t row_bytes, int64_t c, const float (&v)[kPerThread], const F8Scale& s) {
+__device__ inline void store_codes(uint8_t* row, int64_t row_bytes, int64_t c, const float (&v)[kPerThread],
+                                   const F8Scale& s) {
   if (c >= row_bytes) return;
   uint32_t codes[2];
   f8_codes(v, s, codes);
@@ -258,17 +260,21 @@ __global__ __launch_bounds__(kNormThreads) void norm_long_kernel(F8NormParams p)
   const void* again = p.residual ? p.residual_out : p.x;
   const int64_t stride = p.residual ? p.residual_stride : p.x_stride;
   bool first = true;  // the sums are stored once; a thread reads only what it wrote itself
-  const NormFactor f = norm_factor(p, [&](auto sum) {
+  const NormFactor f = norm_factor(p, [&](auto zero) {
+    // A thread adds up to 2^17 chunks one after the other: in fp64, where equal squares would lose up to 2^-7 in fp32.
+    double sum = 0.0;
     for (int64_t q = threadIdx.x; q < chunks; q += blockDim.x) {
       const int left = (int)max(min((int64_t)kPerThread, p.cols - q * kPerThread), (int64_t)0);
       float h[kPerThread];
       if (first) load_h<T>(p, row, q * kPerThread, left, h);
       else load_eight<T>(again, row * stride + q * kPerThread, left, h);
+      decltype(zero) eight = zero;
 #pragma unroll
-      for (int j = 0; j < kPerThread; ++j) sum += (decltype(sum))h[j] * h[j];
+      for (int j = 0; j < kPerThread; ++j) eight += (decltype(zero))h[j] * h[j];
+      sum += eight;
     }
     first = false;
-    return sum;
+    return (decltype(zero))sum;
   });
   for (int64_t q = threadIdx.x; q < chunks; q += blockDim.x) {  // whole blocks: 16 lanes stay together
     const int left = (int)max(min((int64_t)kPerThread, p.cols - q * kPerThread), (int64_t)0);
