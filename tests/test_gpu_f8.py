@@ -460,6 +460,49 @@ def test_results_do_not_depend_on_the_run():
     ex.close()
 
 
+# every tile of the expert passes, most of them with an expert's last tile cut: pairs an expert, and workgroups enough for it
+EXPERT_TILES = [
+    # n, E, k, H, I, skew, holes
+    (700, 8, 2, 4096, 384, True, 0.1),      # down: 256 x 256 and, fp32, 128 x 128
+    (900, 8, 1, 2816, 256, False, 0.0),     # down: 128 x 128
+    (360, 8, 1, 2688, 256, True, 0.0),      # down: 64 x 128
+    (40, 16, 3, 2048, 640, True, 0.0),      # down: 32 x 128
+    (700, 8, 2, 384, 2048, True, 0.1),      # gate+up: 128 rows
+    (900, 8, 1, 256, 2048, False, 0.05),    # gate+up: 128 rows bf16, 64 the others
+    (360, 8, 1, 640, 2688, True, 0.0),      # gate+up: 64 rows
+    (40, 16, 3, 640, 2048, False, 0.0),     # gate+up: 32 rows in two stages
+    (1024, 1, 1, 1280, 256, False, 0.0),    # one expert
+]
+
+
+@pytest.mark.parametrize("part,kind", [("gate_up", "bf16"), ("gate_up", "fp32"), ("gate_up", "e4m3"), ("down", "bf16"),
+                                       ("down", "fp32")])
+@pytest.mark.parametrize("n,E,k,H,I,skew,holes", EXPERT_TILES)
+def test_expert_tiles_match_float64(n, E, k, H, I, skew, holes, part, kind):
+    say(f"expert tiles {part} n={n} E={E} k={k} H={H} I={I} skew={skew} holes={holes} {kind}")
+    ex = Experts(n * 17 + E + H, n, E, k, H, I, skew, holes)
+    ex.check(part, kind)
+    ex.close()
+
+
+@pytest.mark.parametrize("part,H,I", [("down", 4096, 128), ("gate_up", 128, 2048)])
+def test_bad_bins_at_the_large_tiles(part, H, I):
+    say(f"expert tiles, bad bins {part}")
+    n = 700
+    ex = Experts(4, n, 8, 2, H, I)
+    for kind in ("bf16", "fp32"):
+        good = ex.run(part, kind)
+        order = ex.order.astype(np.int32)
+        order[[1, 400]] = [2 * n, -2 ** 31]
+        got, lost = ex.run(part, kind, order=order), ex.order[[1, 400]]
+        keep = np.setdiff1d(np.arange(2 * n), lost)
+        assert np.array_equal(got[keep], good[keep]) and np.all(got[lost] == -7.0)
+        offsets = ex.offsets.copy()
+        offsets[0], offsets[-1] = -5, 2 ** 31 - 1
+        assert np.array_equal(ex.run(part, kind, offsets=offsets), good)
+    ex.close()
+
+
 def test_norm_of_a_very_long_row_of_equal_values():
     import torch
     say("norm of 2^28 equal values")

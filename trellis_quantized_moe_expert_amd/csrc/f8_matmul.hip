@@ -13,6 +13,8 @@
 // as both operands take the same: chunks g and g + 4 of 16.  Four instructions add a block up from zero; its sum then
 // joins the running one by an fp32 multiply-add with the product of the two scales (arbitrary fp32 numbers: the
 // instructions' own scales are powers of two).
+#include <algorithm>
+
 #include "f8_device.h"
 #include "f8_internal.h"
 #include "product_device.h"
@@ -531,30 +533,40 @@ hipError_t launch_tiled(const F8MatmulParams& p, hipStream_t stream, bool launch
   constexpr int threads = KG * WM * WN * 64;
   if (grid * threads > kMostThreads) return hipErrorInvalidConfiguration;
   if (!launch) return hipSuccess;
-  hipLaunchKernelGGL((tiled_kernel<BM, BN, WM, WN, NST, HALVES, EXACT, KG>), dim3((unsigned)grid), dim3(threads), 0, stream,
-                     p, (int)tiles, (int)row_blocks);
+  hipLaunchKernelGGL((tiled_kernel<BM, BN, WM, WN, NST, HALVES, EXACT, KG>), dim3((unsigned)grid), dim3(threads), 0,
+                     stream, p, (int)tiles, (int)row_blocks);
   return hipGetLastError();
 }
 
 // Which kernel and tile.  Large tiles read the operands less often, small ones make more workgroups; below about one
 // workgroup a CU a second group of waves that takes every other stage hides the waits instead.  bf16 results of tiles
-// that wait for the matrix instructions come from the 8-bit ones, all others from the exact ones (see the top).  Times in us at
-// m x n x k, or tokens of a 256-expert, top-6 layer of 4096 x 2048, each side of a border:
+// that wait for the matrix instructions come from the 8-bit ones, all others from the exact ones (see the top).
+// Times in us at m x n x k, or, unless a line says otherwise, of a 256-expert, top-6 layer of 4096 x 2048, each side of
+// a border:
 //   direct up to 16 rows  1 x 4096 x 4096 direct 6.1, 16 x 64 tiles 13.0; 17 rows 10.0, 32 x 64 8.9
 //   256 x 256 from 256    2048 x 8192 x 2048 (256 tiles) 33.8, 128 x 128 46.4; 2048 x 4096 x 4096 (128) 48.8, 41.7
 //   128 x 128 from 400    1024 x 8192 x 2048 (512) 23.6, 64 x 128 28.1; 1024 x 4096 x 4096 (256) 30.1, 26.2
 //   64 x 128 from 160     1000 x 2056 x 4096 (272) 23.0, 32 x 128 25.8, two groups 34; two groups up to 256: 512 x 4096 x
-//                         4096 (256) 16.1, 32 x 128 20.3, one group 21.4; 683 x 2056 x 4064, exact, (187) 24.4, 32 x 128 29.3
+//                         4096 (256) 16.1, 32 x 128 20.3, one group 21.4; 683 x 2056 x 4064, exact, (187) 24.4,
+//                         32 x 128 29.3
 //   32 x 128 from 160     256 x 4096 x 4096 (256) 12.1, 32 x 64 16.4; 128 x 4096 x 4096 (128) 14.5, 9.7; two groups up to
 //                         256: 300 x 2056 x 4064 (170) 16.6, one 19.0
 //   stages of two groups  512 x 4096 x 4096 three 16.1, two 17.7; exact 683 x 2056 x 4064 three 28, two 24.4
 //   exact, large          4096 x 8192 x 8192 128 x 128 493, 64 x 128 570; the 8-bit instructions 240 (256 x 256)
-//   gate+up               24 pairs an expert 32 rows 776, 64 rows 889; 48 pairs 1130, 959; 96 pairs 64 rows 1582, 128 rows 1213
-//                         up to 128 workgroups four stages: 6 pairs (96) 29.8, two 38.2; 24 pairs (384) 78, 73
+// Expert passes take the largest of these tiles that their pairs an expert fill and that makes enough workgroups, both
+// by the average (the bins are on the device; skewed routing makes more tiles of the same pairs):
+//   gate+up               24 pairs an expert 32 rows 776, 64 rows 889; 48 pairs 1130, 959; 96 pairs 64 rows 1582, 128 rows
+//                         1213; workgroups of 128 rows: 128 57, 64 rows 47 (1 expert, 1024 pairs); 192 57, 64 rows 84;
+//                         of 64 rows: 16 15.3, 32 rows 11.0 (1 expert, 100 pairs of 1024 x 1024); 256 47, 32 rows 48
+//                         8-bit, 128 rows: 128 workgroups 38.5, exact 47; 8 13.2, exact 11.0; 24000 pairs of 24 experts
+//                         615, 814
+//                         up to 128 workgroups of 32 rows four stages: 6 pairs (96) 29.8, two 38.2; 24 pairs (384) 78, 73
 //   down                  24 pairs 32 rows 458, 64 rows 461; 48 pairs 64 rows 490, 128 rows 514; 96 pairs 664, 574;
-//                         96 pairs 128 rows 574, 256 rows 609; 192 pairs 970, 717
-// The experts' points are of uniform routing; few or small experts make fewer workgroups than there are CUs, and the
-// rule does not ask.  Without `launch` it says whether the launch could be made.
+//                         96 pairs 128 rows 574, 256 rows 609; 192 pairs 970, 717; workgroups of 256 rows: 96 16.1, 128 rows
+//                         13.8 (8 experts, 6000 pairs of 512 x 1024); 128 35.5, 128 rows 44; of 128 rows: 8 15.1, 32 x 64
+//                         7.4 (1 expert, 100 pairs of 1024 x 1024); 256 26.5, 64 rows 27.4; of 32 x 128: 128 12.9, 32 x 64 of
+//                         two groups 10.5 (8 experts, 120 pairs of 2048 x 2048); 192 13.3, 16.8
+// Without `launch` it says whether the launch could be made.
 template <bool EXACT>
 hipError_t launch_dense(const F8MatmulParams& p, hipStream_t stream, bool launch) {
   constexpr int kDeep = EXACT ? 2 : 3;  // stages of two groups of waves, one workgroup a CU
@@ -575,18 +587,26 @@ hipError_t choose(const F8MatmulParams& p, hipStream_t stream, bool launch) {
     if (p.m <= 16) return launch_direct<8>(p, stream, launch);
     return p.out_bf16 ? launch_dense<false>(p, stream, launch) : launch_dense<true>(p, stream, launch);
   }
-  const int fill = (p.m + p.E - 1) / p.E;  // pairs an expert gets on average
+  const int64_t fill = ((int64_t)p.m + p.E - 1) / p.E;  // pairs an expert gets on average
+  auto groups = [&](int64_t bm, int64_t bn) {
+    return std::min(p.m, p.E) * ((fill + bm - 1) / bm) * ((p.n + bn - 1) / bn);
+  };
   if (p.w1) {
-    if ((int64_t)p.m * (p.n / kF8Block) <= 128) return launch_tiled<32, 256, 1, 4, 4, 2, true>(p, stream, launch);
-    if (fill <= 28) return launch_tiled<32, 256, 1, 4, 2, 2, true>(p, stream, launch);
-    if (fill <= 64) return launch_tiled<64, 256, 1, 4, 2, 2, true>(p, stream, launch);
-    return launch_tiled<128, 256, 2, 4, 2, 2, true>(p, stream, launch);
+    if (p.out_bf16 && fill > 64 && groups(128, 128) >= 128)
+      return launch_tiled<128, 256, 2, 4, 2, 2, false>(p, stream, launch);
+    if (fill > 64 && groups(128, 128) > 160) return launch_tiled<128, 256, 2, 4, 2, 2, true>(p, stream, launch);
+    if (fill > 28 && groups(64, 128) > 160) return launch_tiled<64, 256, 1, 4, 2, 2, true>(p, stream, launch);
+    if (groups(32, 128) > 128) return launch_tiled<32, 256, 1, 4, 2, 2, true>(p, stream, launch);
+    return launch_tiled<32, 256, 1, 4, 4, 2, true>(p, stream, launch);
   }
-  if (fill <= 28) return launch_tiled<32, 128, 1, 4, 2, 1, true>(p, stream, launch);
-  if (fill <= 64) return launch_tiled<64, 128, 1, 4, 2, 1, true>(p, stream, launch);
-  if (!p.out_bf16) return launch_tiled<128, 128, 2, 2, 2, 1, true>(p, stream, launch);
-  if (fill <= 160) return launch_tiled<128, 128, 2, 2, 2, 1, false>(p, stream, launch);
-  return launch_tiled<256, 256, 2, 4, 2, 1, false>(p, stream, launch);
+  if (p.out_bf16 && fill > 160 && groups(256, 256) >= 128)
+    return launch_tiled<256, 256, 2, 4, 2, 1, false>(p, stream, launch);
+  if (fill > 64 && groups(128, 128) > 160)
+    return p.out_bf16 ? launch_tiled<128, 128, 2, 2, 2, 1, false>(p, stream, launch)
+                      : launch_tiled<128, 128, 2, 2, 2, 1, true>(p, stream, launch);
+  if (fill > 28 && groups(64, 128) > 160) return launch_tiled<64, 128, 1, 4, 2, 1, true>(p, stream, launch);
+  if (groups(32, 128) >= 160) return launch_tiled<32, 128, 1, 4, 2, 1, true>(p, stream, launch);
+  return launch_tiled<32, 64, 1, 2, 4, 1, true, 2>(p, stream, launch);
 }
 
 }  // namespace
