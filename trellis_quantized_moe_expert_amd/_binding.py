@@ -218,7 +218,8 @@ _get_device = None  # torch's current device and its stream's handle as plain ca
 _get_stream = None  # against 3.6 through torch.cuda.current_stream()
 _types = {}         # by kind of array (_KINDS): the element types it may have, the usual one first
 _KINDS = {"f": "float32", "i": "int32", "b": "bfloat16 int16 uint16", "h": "float16 int16 uint16",
-          "u": "uint8 int8 float4_e2m1fn_x2 float8_e8m0fnu", "e": "uint8 int8 float8_e4m3fn"}  # 16-bit values may come as their bits
+          "u": "uint8 int8 float4_e2m1fn_x2 float8_e8m0fnu",  # 16-bit values may come as their bits
+          "e": "uint8 int8 float8_e4m3fn"}
 
 
 def _find_torch() -> bool:
@@ -622,7 +623,7 @@ def qtip_moe_forward_gated(plan, weights: qtip_moe_weights, gate: qtip_moe_gate,
 
 
 def _check_rows(fn: str, name: str, kind: str, obj, rows: int, cols: int, row_stride: int) -> None:
-    """A tensor of a kind that holds `rows` rows of cols elements, row_stride apart: rows of a wider tensor are welcome."""
+    """A tensor of a kind with `rows` rows of cols elements, row_stride apart: rows of a wider tensor are welcome."""
     if not ((_torch is not None or _find_torch()) and isinstance(obj, _torch.Tensor)):
         return
     if obj.get_device() < 0 or obj.get_device() != _get_device():
@@ -720,7 +721,8 @@ def qtip_f8_rms_norm(x, type_, rows, cols, x_stride, residual, residual_stride, 
         names, kinds, objs, sizes = (*names, "values"), kinds + kind, (*objs, values), (*sizes, whole)
     if x_stride == cols and (not summed or residual_stride == cols):  # whole arrays all of them
         if summed:
-            names, kinds, objs = ("x", "residual", "residual_out", *names), kind * 3 + kinds, (x, residual, residual_out, *objs)
+            names, kinds = ("x", "residual", "residual_out", *names), kind * 3 + kinds
+            objs = x, residual, residual_out, *objs
             p = _pointers(fn, kinds, names, objs, (whole, whole, whole, *sizes))
         else:
             p = _pointers(fn, kind + kinds, ("x", *names), (x, *objs), (whole, *sizes))

@@ -15,9 +15,9 @@ harmless.  After compiling, the build scans the device assembly and fails if any
 instruction appears, so the property is checked on every build, not assumed.
 
 Machine verifier: the sources but those of UNVERIFIED are compiled with
-`-mllvm -verify-machineinstrs`, so that wrong code of the compiler's own passes ends the build.  It is there because of a case: with a fragment loaded under a condition and used in a
-loop, the pass that forms memory clauses lost track of the fragment's registers, and an address was written over
-them.  The verifier changes no code.
+`-mllvm -verify-machineinstrs`, so that wrong code of the compiler's own passes ends the build.  It is there because
+of a case: with a fragment loaded under a condition and used in a loop, the pass that forms memory clauses lost track
+of the fragment's registers, and an address was written over them.  The verifier changes no code.
 """
 from __future__ import annotations
 
@@ -52,7 +52,8 @@ def hipcc() -> str:
 
 def compile_command(src: str, obj: str) -> list:
     return [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall", *DEVICE_FLAGS,
-            *([] if src in UNVERIFIED else VERIFY), *SOURCE_FLAGS.get(src, []), "-save-temps=obj", "-c", os.path.join(_HERE, src), "-o", obj]
+            *([] if src in UNVERIFIED else VERIFY), *SOURCE_FLAGS.get(src, []), "-save-temps=obj", "-c",
+            os.path.join(_HERE, src), "-o", obj]
 
 
 def link_command(objs: list, output: str) -> list:

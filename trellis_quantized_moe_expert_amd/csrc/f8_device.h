@@ -2,7 +2,8 @@
 //
 //   amax rule: scale = amax / 448 rounded to fp32      (448 = 1.75 * 2^8, the largest code)
 //   pow2 rule: scale = the smallest power of two that is no less than amax / 448
-//   both at least 2^-126, so that 1 / scale is an fp32 number; code = the e4m3 value nearest to x / scale, a tie the even one
+//   both at least 2^-126, so that 1 / scale is an fp32 number
+//   code = the e4m3 value nearest to x / scale, a tie the even one
 //
 // |x| / scale is at most 448 (1 + 2^-23), which rounds to 448: no code needs to be cut.
 #pragma once
