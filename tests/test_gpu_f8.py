@@ -467,8 +467,9 @@ EXPERT_TILES = [
     (900, 8, 1, 2816, 256, False, 0.0),     # down: 128 x 128
     (360, 8, 1, 2688, 256, True, 0.0),      # down: 64 x 128
     (40, 16, 3, 2048, 640, True, 0.0),      # down: 32 x 128
-    (700, 8, 2, 384, 2048, True, 0.1),      # gate+up: 128 rows
+    (700, 8, 2, 384, 2048, True, 0.1),      # gate+up: 256 rows bf16, 128 the others
     (900, 8, 1, 256, 2048, False, 0.05),    # gate+up: 128 rows bf16, 64 the others
+    (1000, 8, 1, 1152, 2048, True, 0.0),    # the same over more stages
     (360, 8, 1, 640, 2688, True, 0.0),      # gate+up: 64 rows
     (40, 16, 3, 640, 2048, False, 0.0),     # gate+up: 32 rows in two stages
     (1024, 1, 1, 1280, 256, False, 0.0),    # one expert
@@ -482,6 +483,14 @@ def test_expert_tiles_match_float64(n, E, k, H, I, skew, holes, part, kind):
     say(f"expert tiles {part} n={n} E={E} k={k} H={H} I={I} skew={skew} holes={holes} {kind}")
     ex = Experts(n * 17 + E + H, n, E, k, H, I, skew, holes)
     ex.check(part, kind)
+    ex.close()
+
+
+@pytest.mark.parametrize("n,I", [(900, 2048), (1100, 3328)])
+def test_gate_up_tiles_over_more_stages_than_a_register_holds_scales_for(n, I):
+    say(f"expert tiles gate_up {n} pairs of one expert, 8448 inputs, {I} outputs")
+    ex = Experts(n, n, 1, 1, 8448, I)
+    ex.check("gate_up", "bf16")
     ex.close()
 
 

@@ -559,7 +559,8 @@ hipError_t launch_tiled(const F8MatmulParams& p, hipStream_t stream, bool launch
 //                         1213; workgroups of 128 rows: 128 57, 64 rows 47 (1 expert, 1024 pairs); 192 57, 64 rows 84;
 //                         of 64 rows: 16 15.3, 32 rows 11.0 (1 expert, 100 pairs of 1024 x 1024); 256 47, 32 rows 48
 //                         8-bit, 128 rows: 128 workgroups 38.5, exact 47; 8 13.2, exact 11.0; 24000 pairs of 24 experts
-//                         615, 814
+//                         in three stages 532, in two 616, exact 814, 256 rows 438; workgroups of 256 rows: 96 50, 128
+//                         rows 33 (1 expert, 3000 pairs of 1024 x 4096); 128 65, 128 rows 75 (8 experts, 2000 pairs)
 //                         up to 128 workgroups of 32 rows four stages: 6 pairs (96) 29.8, two 38.2; 24 pairs (384) 78, 73
 //   down                  24 pairs 32 rows 458, 64 rows 461; 48 pairs 64 rows 490, 128 rows 514; 96 pairs 664, 574;
 //                         96 pairs 128 rows 574, 256 rows 609; 192 pairs 970, 717; workgroups of 256 rows: 96 16.1, 128 rows
@@ -592,8 +593,10 @@ hipError_t choose(const F8MatmulParams& p, hipStream_t stream, bool launch) {
     return std::min(p.m, p.E) * ((fill + bm - 1) / bm) * ((p.n + bn - 1) / bn);
   };
   if (p.w1) {
+    if (p.out_bf16 && fill > 160 && groups(256, 128) >= 128)
+      return launch_tiled<256, 256, 2, 4, 2, 2, false>(p, stream, launch);
     if (p.out_bf16 && fill > 64 && groups(128, 128) >= 128)
-      return launch_tiled<128, 256, 2, 4, 2, 2, false>(p, stream, launch);
+      return launch_tiled<128, 256, 2, 4, 3, 2, false>(p, stream, launch);
     if (fill > 64 && groups(128, 128) > 160) return launch_tiled<128, 256, 2, 4, 2, 2, true>(p, stream, launch);
     if (fill > 28 && groups(64, 128) > 160) return launch_tiled<64, 256, 1, 4, 2, 2, true>(p, stream, launch);
     if (groups(32, 128) > 128) return launch_tiled<32, 256, 1, 4, 2, 2, true>(p, stream, launch);
