@@ -460,11 +460,19 @@ def test_results_do_not_depend_on_the_run():
     ex.close()
 
 
+@pytest.mark.parametrize("m,n,k", [(1030, 6500, 160), (1500, 4702, 1040), (1153, 5120, 8352), (1281, 5001, 400)])
+def test_product_of_wide_tiles_matches_float64(m, n, k):
+    say(f"product of 128 x 256 tiles {m}x{n}x{k}")
+    rng = np.random.default_rng(m + n + k)
+    check_product(packed(rng, m, k, 1, -6, -3), packed(rng, n, k, 128, -6, -3), "bf16")
+
+
 # every tile of the expert passes, most of them with an expert's last tile cut: pairs an expert, and workgroups enough for it
 EXPERT_TILES = [
     # n, E, k, H, I, skew, holes
     (700, 8, 2, 4096, 384, True, 0.1),      # down: 256 x 256 and, fp32, 128 x 128
     (900, 8, 1, 2816, 256, False, 0.0),     # down: 128 x 128
+    (900, 8, 1, 2816, 1152, True, 0.05),    # down: 128 x 256 bf16
     (360, 8, 1, 2688, 256, True, 0.0),      # down: 64 x 128
     (40, 16, 3, 2048, 640, True, 0.0),      # down: 32 x 128
     (700, 8, 2, 384, 2048, True, 0.1),      # gate+up: 256 rows bf16, 128 the others

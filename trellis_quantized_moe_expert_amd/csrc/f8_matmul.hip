@@ -544,8 +544,10 @@ hipError_t launch_tiled(const F8MatmulParams& p, hipStream_t stream, bool launch
 // Times in us at m x n x k, or, unless a line says otherwise, of a 256-expert, top-6 layer of 4096 x 2048, each side of
 // a border:
 //   direct up to 16 rows  1 x 4096 x 4096 direct 6.1, 16 x 64 tiles 13.0; 17 rows 10.0, 32 x 64 8.9
-//   256 x 256 from 256    2048 x 8192 x 2048 (256 tiles) 33.8, 128 x 128 46.4; 2048 x 4096 x 4096 (128) 48.8, 41.7
-//   128 x 128 from 400    1024 x 8192 x 2048 (512) 23.6, 64 x 128 28.1; 1024 x 4096 x 4096 (256) 30.1, 26.2
+//   256 x 256 from 256    2048 x 8192 x 2048 (256 tiles) 33.7, 128 x 256 40.3; 2048 x 4096 x 4096 (128) 46, 35.7
+//   128 x 256 from 200    three stages: 1500 x 5120 x 4096 (240) 34.1, 128 x 128 39.3; 1024 x 4096 x 4096 (128) 29.3, two
+//                         groups of 64 x 128 25.0; 1024 x 8192 x 2048 (256) 22.2, 128 x 128 23.8, 64 x 128 28.1
+//   exact, 128 x 128 from 400 tiles
 //   64 x 128 from 160     1000 x 2056 x 4096 (272) 23.0, 32 x 128 25.8, two groups 34; two groups up to 256: 512 x 4096 x
 //                         4096 (256) 16.1, 32 x 128 20.3, one group 21.4; 683 x 2056 x 4064, exact, (187) 24.4,
 //                         32 x 128 29.3
@@ -567,6 +569,9 @@ hipError_t launch_tiled(const F8MatmulParams& p, hipStream_t stream, bool launch
 //                         13.8 (8 experts, 6000 pairs of 512 x 1024); 128 35.5, 128 rows 44; of 128 rows: 8 15.1, 32 x 64
 //                         7.4 (1 expert, 100 pairs of 1024 x 1024); 256 26.5, 64 rows 27.4; of 32 x 128: 128 12.9, 32 x 64 of
 //                         two groups 10.5 (8 experts, 120 pairs of 2048 x 2048); 192 13.3, 16.8
+//                         8-bit: 83 pairs 128 x 256 57.5, 128 x 128 63.7 (24 experts, 2000 pairs); 1024 inputs 18.1, 18.8 (8
+//                         experts, 1100 pairs of 4096), 512 inputs 26.4, 24.0 (64 experts, 5400 pairs of 2048); 128
+//                         workgroups of 128 x 128 20.3, exact 64 x 128 23.8 (8 experts, 900 pairs of 2048 x 2048)
 // Without `launch` it says whether the launch could be made.
 template <bool EXACT>
 hipError_t launch_dense(const F8MatmulParams& p, hipStream_t stream, bool launch) {
@@ -574,8 +579,10 @@ hipError_t launch_dense(const F8MatmulParams& p, hipStream_t stream, bool launch
   auto groups = [&](int64_t bm, int64_t bn) { return (p.m + bm - 1) / bm * ((p.n + bn - 1) / bn); };
   if constexpr (!EXACT) {
     if (groups(256, 256) >= 256) return launch_tiled<256, 256, 2, 4, 2, 1, false>(p, stream, launch);
+    if (groups(128, 256) >= 200) return launch_tiled<128, 256, 2, 4, 3, 1, false>(p, stream, launch);
+  } else {
+    if (groups(128, 128) >= 400) return launch_tiled<128, 128, 2, 2, 2, 1, true>(p, stream, launch);
   }
-  if (groups(128, 128) >= 400) return launch_tiled<128, 128, 2, 2, 2, 1, EXACT>(p, stream, launch);
   if (groups(64, 128) > 256) return launch_tiled<64, 128, 1, 4, 2, 1, EXACT>(p, stream, launch);
   if (groups(64, 128) >= 160) return launch_tiled<64, 128, 2, 2, kDeep, 1, EXACT, 2>(p, stream, launch);
   if (groups(32, 128) > 256) return launch_tiled<32, 128, 1, 4, 2, 1, EXACT>(p, stream, launch);
@@ -604,9 +611,10 @@ hipError_t choose(const F8MatmulParams& p, hipStream_t stream, bool launch) {
   }
   if (p.out_bf16 && fill > 160 && groups(256, 256) >= 128)
     return launch_tiled<256, 256, 2, 4, 2, 1, false>(p, stream, launch);
-  if (fill > 64 && groups(128, 128) > 160)
-    return p.out_bf16 ? launch_tiled<128, 128, 2, 2, 2, 1, false>(p, stream, launch)
-                      : launch_tiled<128, 128, 2, 2, 2, 1, true>(p, stream, launch);
+  if (p.out_bf16 && fill > 64 && groups(128, 128) >= 128)
+    return p.k > 4 * kF8Block ? launch_tiled<128, 256, 2, 4, 3, 1, false>(p, stream, launch)
+                              : launch_tiled<128, 128, 2, 2, 2, 1, false>(p, stream, launch);
+  if (fill > 64 && groups(128, 128) > 160) return launch_tiled<128, 128, 2, 2, 2, 1, true>(p, stream, launch);
   if (fill > 28 && groups(64, 128) > 160) return launch_tiled<64, 128, 1, 4, 2, 1, true>(p, stream, launch);
   if (groups(32, 128) >= 160) return launch_tiled<32, 128, 1, 4, 2, 1, true>(p, stream, launch);
   return launch_tiled<32, 64, 1, 2, 4, 1, true, 2>(p, stream, launch);
