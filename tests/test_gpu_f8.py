@@ -460,7 +460,8 @@ def test_results_do_not_depend_on_the_run():
     ex.close()
 
 
-@pytest.mark.parametrize("m,n,k", [(1030, 6500, 160), (1500, 4702, 1040), (1153, 5120, 8352), (1281, 5001, 400)])
+@pytest.mark.parametrize("m,n,k", [(1030, 6500, 160), (1500, 4702, 1040), (1153, 5120, 8352), (1281, 5001, 400), (1540, 4099, 1040),
+                                   (1154, 5123, 1040), (2500, 4100, 288)])
 def test_product_of_wide_tiles_matches_float64(m, n, k):
     say(f"product of 128 x 256 tiles {m}x{n}x{k}")
     rng = np.random.default_rng(m + n + k)

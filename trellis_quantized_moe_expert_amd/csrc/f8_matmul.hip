@@ -544,10 +544,12 @@ hipError_t launch_tiled(const F8MatmulParams& p, hipStream_t stream, bool launch
 // Times in us at m x n x k, or, unless a line says otherwise, of a 256-expert, top-6 layer of 4096 x 2048, each side of
 // a border:
 //   direct up to 16 rows  1 x 4096 x 4096 direct 6.1, 16 x 64 tiles 13.0; 17 rows 10.0, 32 x 64 8.9
-//   256 x 256 from 256    2048 x 8192 x 2048 (256 tiles) 33.7, 128 x 256 40.3; 2048 x 4096 x 4096 (128) 46, 35.7
+//   256 x 256             where tiles of 128 x 256 take a second turn on 256 CUs: 2500 x 4096 x 2048 (320 of those) 27.4,
+//                         128 x 256 36.1; 1792 x 8192 x 4096 (448) 54.3, 64.5; 2048 x 4096 x 4096 (256) 46, 35.7
 //   128 x 256 from 200    three stages: 1500 x 5120 x 4096 (240) 34.1, 128 x 128 39.3; 1024 x 4096 x 4096 (128) 29.3, two
-//                         groups of 64 x 128 25.0; 1024 x 8192 x 2048 (256) 22.2, 128 x 128 23.8, 64 x 128 28.1
-//   exact, 128 x 128 from 400 tiles
+//                         groups of 64 x 128 25.0; 1024 x 8192 x 2048 (256) 22.2, 128 x 128 23.8, 64 x 128 28.1; of 512
+//                         inputs 4096 x 2048 x 512 (256) 11.3, 128 x 128 10.6
+//   128 x 128 from 400    (these, and exact)
 //   64 x 128 from 160     1000 x 2056 x 4096 (272) 23.0, 32 x 128 25.8, two groups 34; two groups up to 256: 512 x 4096 x
 //                         4096 (256) 16.1, 32 x 128 20.3, one group 21.4; 683 x 2056 x 4064, exact, (187) 24.4,
 //                         32 x 128 29.3
@@ -578,11 +580,11 @@ hipError_t launch_dense(const F8MatmulParams& p, hipStream_t stream, bool launch
   constexpr int kDeep = EXACT ? 2 : 3;  // stages of two groups of waves, one workgroup a CU
   auto groups = [&](int64_t bm, int64_t bn) { return (p.m + bm - 1) / bm * ((p.n + bn - 1) / bn); };
   if constexpr (!EXACT) {
-    if (groups(256, 256) >= 256) return launch_tiled<256, 256, 2, 4, 2, 1, false>(p, stream, launch);
-    if (groups(128, 256) >= 200) return launch_tiled<128, 256, 2, 4, 3, 1, false>(p, stream, launch);
-  } else {
-    if (groups(128, 128) >= 400) return launch_tiled<128, 128, 2, 2, 2, 1, true>(p, stream, launch);
+    if (groups(128, 256) > 256) return launch_tiled<256, 256, 2, 4, 2, 1, false>(p, stream, launch);
+    if (groups(128, 256) >= 200 && p.k > 4 * kF8Block)
+      return launch_tiled<128, 256, 2, 4, 3, 1, false>(p, stream, launch);
   }
+  if (groups(128, 128) >= 400) return launch_tiled<128, 128, 2, 2, 2, 1, EXACT>(p, stream, launch);
   if (groups(64, 128) > 256) return launch_tiled<64, 128, 1, 4, 2, 1, EXACT>(p, stream, launch);
   if (groups(64, 128) >= 160) return launch_tiled<64, 128, 2, 2, kDeep, 1, EXACT, 2>(p, stream, launch);
   if (groups(32, 128) > 256) return launch_tiled<32, 128, 1, 4, 2, 1, EXACT>(p, stream, launch);

@@ -82,7 +82,8 @@ __device__ inline int tile_row(const P& p, int start, int len, int i) {
 }
 
 // Stores SPAN neighbouring outputs of row r from column c on: a whole vector where p.n is a multiple
-// of SPAN (so that it lies in the row or past it, aligned), one by one otherwise.
+// of SPAN (so that it lies in the row or past it, aligned); otherwise a vector at any element's address, and one by one
+// at the row's end.
 template <int SPAN, class P>
 __device__ inline void store_bf16(const P& p, int r, int c, const float (&v)[SPAN]) {
   if (c >= p.n) return;
@@ -102,9 +103,27 @@ __device__ inline void store_f32(const P& p, int r, int c, const float (&v)[SPAN
   for (int i = 0; i < SPAN; i += 4) *reinterpret_cast<float4*>(d + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
 }
 
+template <class E, int SPAN>
+struct __attribute__((packed, aligned(sizeof(E)))) Neighbours {
+  E e[SPAN];
+};
+
+template <class E, int SPAN>
+__device__ inline void store_neighbours(void* out, size_t o, const float (&v)[SPAN]) {
+  Neighbours<E, SPAN> w;
+#pragma unroll
+  for (int i = 0; i < SPAN; ++i) w.e[i] = (E)v[i];
+  *reinterpret_cast<Neighbours<E, SPAN>*>(reinterpret_cast<E*>(out) + o) = w;
+}
+
 template <int SPAN, class P>
 __device__ inline void store_odd(const P& p, int r, int c, const float (&v)[SPAN]) {
   const size_t o = (size_t)r * p.n + c;
+  if (p.n - c >= SPAN) {
+    if (p.out_bf16) store_neighbours<__bf16>(p.out, o, v);
+    else store_neighbours<float>(p.out, o, v);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < SPAN; ++i) {
     if (c + i >= p.n) break;
