@@ -610,8 +610,8 @@ typedef struct qtip_f8_weights {
  * outside [0, n k) skipped, so device-side garbage cannot reach memory out of bounds; what a pair
  * that two bins name gets is unspecified.  Only the pass's own weights are read; the others may be NULL.  Codes and
  * out 16-byte aligned, scales 4-byte aligned; the plan gives E, k, H, I and max_tokens; its rung, arm
- * and variant do not matter.  Errors as qtip_moe_forward; a bad pass or out_dtype, out_scales missing or not
- * wanted -> INVALID_ARG. */
+ * and variant do not matter.  The inputs of a pass (H, or I of the down pass) must be below 2^23.  Errors as
+ * qtip_moe_forward; a bad pass or out_dtype, out_scales missing or not wanted, too many inputs -> INVALID_ARG. */
 enum { QTIP_F8_PASS_GATE_UP = 0, QTIP_F8_PASS_DOWN = 1 };
 qtip_status qtip_f8_expert_matmul(qtip_moe_plan_t plan, int32_t pass, const qtip_f8_weights* w /*host struct*/,
                                   const uint8_t* a_codes, const float* a_scales, const int32_t* offsets,
@@ -623,7 +623,8 @@ qtip_status qtip_f8_expert_matmul(qtip_moe_plan_t plan, int32_t pass, const qtip
  * [n][H], scales [n][H/128].  y = h Wd^T in fp32; out[t] = sum_j w[t,j] y(t, j) in fp32, j ascending, cast to the
  * plan's out_dtype.  Left-out slots add nothing.  workspace: qtip_f8_moe_workspace_bytes(plan) bytes,
  * 256-byte aligned, contents need no initialisation; two calls, or replays of two captured graphs,
- * that may overlap need one each.  Errors as qtip_moe_forward; a bad gate -> INVALID_ARG. */
+ * that may overlap need one each.  H and I must be below 2^23.  Errors as qtip_moe_forward; a bad gate, too
+ * large an H or I -> INVALID_ARG. */
 size_t qtip_f8_moe_workspace_bytes(qtip_moe_plan_t plan);
 qtip_status qtip_f8_moe_forward(qtip_moe_plan_t plan, const qtip_f8_weights* w /*host struct of device ptrs*/,
                                 const qtip_moe_gate* gate /*host struct or NULL*/, const uint8_t* x_codes,

@@ -1171,6 +1171,15 @@ qtip_status check_f8_pass(int32_t pass, const qtip_f8_weights* w) {
   return QTIP_OK;
 }
 
+// The kernels address a tile's rows of a matrix, up to 256, by 31-bit offsets.
+constexpr int32_t kF8MostInputs = 1 << 23;
+
+qtip_status check_f8_inputs(const qtip_moe_plan_s* plan, int32_t pass) {
+  const bool gu = pass == QTIP_F8_PASS_GATE_UP;
+  if ((gu ? plan->d.hidden : plan->d.inter) < kF8MostInputs) return QTIP_OK;
+  return fail(QTIP_ERR_INVALID_ARG, gu ? "hidden must be below 2^23 for e4m3 experts" : "inter must be below 2^23 for e4m3 experts");
+}
+
 F8MatmulParams f8_pass_params(const qtip_moe_plan_s* plan, int32_t pass, const qtip_f8_weights* w,
                               const uint8_t* a_codes, const float* a_scales, const int32_t* offsets,
                               const int32_t* sorted_pair, int32_t n_tokens, void* out, int32_t out_dtype,
@@ -1765,7 +1774,7 @@ qtip_status qtip_f8_matmul(const uint8_t* a_codes, const float* a_scales, int32_
   if (out_dtype != QTIP_OUT_BF16 && out_dtype != QTIP_OUT_F32) return fail(QTIP_ERR_INVALID_ARG, "unknown out_dtype");
   if (m < 1 || n < 1 || k < 1) return fail(QTIP_ERR_INVALID_CONFIG, "m, n and k must be >= 1 (an empty launch is an error)");
   if (k % 16) return fail(QTIP_ERR_INVALID_ARG, "k must be a multiple of 16");
-  if (k >= 1 << 23 || (int64_t)m * k >= ((int64_t)1 << 37) || (int64_t)n * k >= ((int64_t)1 << 37) ||
+  if (k >= kF8MostInputs || (int64_t)m * k >= ((int64_t)1 << 37) || (int64_t)n * k >= ((int64_t)1 << 37) ||
       (int64_t)m * n >= ((int64_t)1 << 40))
     return fail(QTIP_ERR_INVALID_ARG, "k must be below 2^23, m * k and n * k below 2^37, m * n below 2^40");
   if (!f8_aligned(a_codes, a_scales) || !f8_aligned(w_codes, w_scales) || (reinterpret_cast<uintptr_t>(out) & 15))
@@ -1807,6 +1816,7 @@ qtip_status qtip_f8_expert_matmul(qtip_moe_plan_t plan, int32_t pass, const qtip
     return fail(QTIP_ERR_INVALID_ARG, "out_scales must be given with QTIP_OUT_E4M3 and be NULL otherwise");
   if (!f8_aligned(a_codes, a_scales) || !f8_aligned(out, out_scales))
     return fail(QTIP_ERR_INVALID_ARG, "codes and out must be 16-byte aligned, scales 4-byte aligned");
+  if ((s = check_f8_inputs(plan, pass)) != QTIP_OK) return s;
   if (n_tokens <= 0 || n_tokens > plan->d.max_tokens)
     return fail(QTIP_ERR_INVALID_CONFIG, "n_tokens must be in [1, max_tokens] (an empty launch is an error)");
   const hipStream_t st = (hipStream_t)stream;
@@ -1831,6 +1841,8 @@ qtip_status qtip_f8_moe_forward(qtip_moe_plan_t plan, const qtip_f8_weights* w, 
   if (gate && (s = check_gate(plan, gate)) != QTIP_OK) return s;
   if (!f8_aligned(x_codes, x_scales) || (reinterpret_cast<uintptr_t>(out) & 15))
     return fail(QTIP_ERR_INVALID_ARG, "x_codes and out must be 16-byte aligned, x_scales 4-byte aligned");
+  if ((s = check_f8_inputs(plan, QTIP_F8_PASS_GATE_UP)) != QTIP_OK) return s;
+  if ((s = check_f8_inputs(plan, QTIP_F8_PASS_DOWN)) != QTIP_OK) return s;
   if (n_tokens <= 0 || n_tokens > plan->d.max_tokens)
     return fail(QTIP_ERR_INVALID_CONFIG, "n_tokens must be in [1, max_tokens] (an empty launch is an error)");
   const qtip_moe_desc& d = plan->d;

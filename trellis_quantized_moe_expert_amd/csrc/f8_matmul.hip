@@ -234,7 +234,8 @@ __global__ __launch_bounds__(KG * WM * WN * 64) void tiled_kernel(F8MatmulParams
   };
 
   // Dense activations are addressed from the tile's first row, gathered ones from row 0 (a plan keeps them under
-  // 2^30 bytes); their scales, a thirty-second of the codes, likewise.
+  // 2^30 bytes); their scales, a thirty-second of the codes, likewise.  Weights are addressed from the tile's first
+  // row: k is below 2^23, so that 256 rows stay below the buffer's 2^31 bytes.
   const int a_base = p.offsets ? 0 : start;
   const size_t w_base = ((size_t)expert * p.n + n0) * p.k;
   const uint8_t* const a_codes = p.a + (size_t)a_base * p.k;
