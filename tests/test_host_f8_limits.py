@@ -36,3 +36,15 @@ def test_expert_passes_refuse_more_inputs_than_a_tile_can_address(hidden, inter)
         for n in (0, 1):
             assert layer(n) == ARG and "2^23" in q.last_error_detail()
     q.qtip_moe_plan_destroy(plan)
+
+
+def test_quantisation_of_128_rows_a_block_takes_fewer_than_2_24_blocks():
+    def detail(rows, cols):
+        # codes that are not aligned: what the sizes let through is refused for that
+        assert q.raw_status("qtip_f8_quantize", 256, q.QTIP_F8_BF16, rows, cols, cols, 128, q.QTIP_F8_SCALE_AMAX, 264, 256,
+                            None) == ARG
+        return q.last_error_detail()
+    for rows, cols in ((1 << 29, 1), ((1 << 29) + 130, 128), (2 ** 31 - 128, 1), ((1 << 18) - 128, 1 << 20)):
+        assert "aligned" in detail(rows, cols), (rows, cols)
+    for rows, cols in ((2 ** 31 - 127, 1), (2 ** 31 - 1, 128), (1 << 18, 1 << 20)):
+        assert "blocks" in detail(rows, cols), (rows, cols)

@@ -1694,7 +1694,8 @@ qtip_status qtip_f8_quantize(const void* src, int32_t src_type, int32_t rows, in
   if (rows < 1 || cols < 1) return fail(QTIP_ERR_INVALID_CONFIG, "rows and cols must be >= 1 (an empty launch is an error)");
   if (row_stride < cols || row_stride >= ((int64_t)1 << 40))
     return fail(QTIP_ERR_INVALID_ARG, "row_stride must be at least cols and below 2^40");
-  // 16 threads a block of a row, 256 a block of 128 rows; whole workgroups, below 2^32 threads
+  // 16 threads a block of a row, whole workgroups, below 2^32 threads; blocks of 128 rows take as many launches as they
+  // need
   const int64_t blocks = ((int64_t)cols + kF8Block - 1) / kF8Block;
   if (block_rows == 1 ? rows * blocks > ((int64_t)1 << 28) - 16
                       : ((int64_t)rows + kF8Block - 1) / kF8Block * blocks >= ((int64_t)1 << 24))

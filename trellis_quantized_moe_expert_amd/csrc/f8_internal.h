@@ -24,6 +24,7 @@ struct F8QuantParams {
   int32_t pow2;        // scale rule
   uint8_t* codes;      // [rows][f8_row_bytes(cols)]
   float* scales;       // [ceil(rows / block_rows)][ceil(cols / 128)]
+  uint32_t first;      // the 128 x 128 block that a launch begins with; launch_f8_quantize sets it
 };
 
 hipError_t launch_f8_quantize(const F8QuantParams& p, hipStream_t stream);

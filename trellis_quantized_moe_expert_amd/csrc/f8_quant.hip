@@ -105,14 +105,15 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_rows_kernel(F8QuantPar
 // A workgroup a block, its values in registers: 16 threads a row, each with two rows.  8192 x 8136 fp32: 69 us, 4.8 TB/s;
 // with 256 threads of eight rows each 76, with 512 74: fewer waves have less asked for at a time.
 constexpr int kTileThreads = 1024;
+constexpr int64_t kMostTiles = UINT32_MAX / kTileThreads;  // of a launch, which has below 2^32 threads
 
 template <class T>
 __global__ __launch_bounds__(kTileThreads) void quantize_tile_kernel(F8QuantParams p) {
   constexpr int kRowsAtOnce = kTileThreads / 16, kSteps = kF8Block / kRowsAtOnce;
   __shared__ uint32_t tops[kTileThreads / 64];
   const uint32_t blocks = ((uint32_t)p.cols + kF8Block - 1) / kF8Block;
-  const uint32_t br = blockIdx.x / blocks;
-  const int64_t c = (int64_t)(blockIdx.x - br * blocks) * kF8Block + (threadIdx.x & 15) * kPerThread;
+  const uint32_t block = p.first + blockIdx.x, br = block / blocks;  // below 2^24
+  const int64_t c = (int64_t)(block - br * blocks) * kF8Block + (threadIdx.x & 15) * kPerThread;
   const int64_t row0 = (int64_t)br * kF8Block + (threadIdx.x >> 4);
   const int left = (int)min((int64_t)kPerThread, p.cols - c);
   float v[kSteps][kPerThread];
@@ -138,18 +139,23 @@ __global__ __launch_bounds__(kTileThreads) void quantize_tile_kernel(F8QuantPara
     const int64_t row = row0 + i * kRowsAtOnce;
     if (row < p.rows) store_codes(p.codes + row * row_bytes, row_bytes, c, v[i], s);
   }
-  if (threadIdx.x == 0) p.scales[blockIdx.x] = s.scale;
+  if (threadIdx.x == 0) p.scales[block] = s.scale;
 }
 
 template <class T>
-void launch_quantize_type(const F8QuantParams& p, hipStream_t stream) {
+void launch_quantize_type(F8QuantParams p, hipStream_t stream) {
   const int64_t blocks = ((int64_t)p.cols + kF8Block - 1) / kF8Block;
   if (p.block_rows == 1) {
     const int64_t grid = (blocks * 16 * p.rows + kQuantThreads - 1) / kQuantThreads;
     hipLaunchKernelGGL((quantize_rows_kernel<T>), dim3((unsigned)grid), dim3(kQuantThreads), 0, stream, p);
   } else {
-    const int64_t grid = blocks * (((int64_t)p.rows + kF8Block - 1) / kF8Block);
-    hipLaunchKernelGGL((quantize_tile_kernel<T>), dim3((unsigned)grid), dim3(kTileThreads), 0, stream, p);
+    // many rows of few columns have more blocks than a launch: the next one takes them on
+    const int64_t all = blocks * (((int64_t)p.rows + kF8Block - 1) / kF8Block);
+    for (int64_t first = 0; first < all; first += kMostTiles) {
+      p.first = (uint32_t)first;
+      const int64_t grid = all - first < kMostTiles ? all - first : kMostTiles;
+      hipLaunchKernelGGL((quantize_tile_kernel<T>), dim3((unsigned)grid), dim3(kTileThreads), 0, stream, p);
+    }
   }
 }
 
