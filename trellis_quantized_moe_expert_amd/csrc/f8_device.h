@@ -68,7 +68,9 @@ __device__ inline float f8_settle(float q, float x, float scale) {
 }
 
 // Codes of N values (a multiple of 4), four to a dword.  The products with the rounded inverse are within
-// 2 units of the last place; about one value in 65536 is next to a border and makes its wave look again.
+// 2 units of the last place.  A wave looks again where one of its values is next to a number with its low 19 bits
+// clear: a border (about one value in 65536), but also a code, zero among them.  By the amax rule a block's largest
+// value is next to 448, so all waves look again; by powers of two the products are exact and none does.
 template <int N>
 __device__ inline void f8_codes(const float (&x)[N], const F8Scale& s, uint32_t (&codes)[N / 4]) {
   float q[N];

@@ -558,6 +558,9 @@ hipError_t launch_tiled(const F8MatmulParams& p, hipStream_t stream, bool launch
 //                         256: 300 x 2056 x 4064 (170) 16.6, one 19.0
 //   stages of two groups  512 x 4096 x 4096 three 16.1, two 17.7; exact 683 x 2056 x 4064 three 28, two 24.4
 //   exact, large          4096 x 8192 x 8192 128 x 128 493, 64 x 128 570; the 8-bit instructions 240 (256 x 256)
+// These rules ask for workgroups, not whether m and n fill a tile.  Where one of the two is small and the other very
+// large they take too large a tile: 32 x 129280 x 7168 256 x 256 194, 128 x 256 161, 32 x 128 180, exact 128 x 128 223,
+// 32 x 128 185; 128 x 129280 x 7168 256 x 256 220, 128 x 256 200; 65536 x 32 x 4096 256 x 256 74, 128 x 128 69.
 // Expert passes take the largest of these tiles that their pairs an expert fill and that makes enough workgroups, both
 // by the average (the bins are on the device; skewed routing makes more tiles of the same pairs):
 //   gate+up               24 pairs an expert 32 rows 776, 64 rows 889; 48 pairs 1130, 959; 96 pairs 64 rows 1582, 128 rows

@@ -162,7 +162,8 @@ void launch_quantize_type(F8QuantParams p, hipStream_t stream) {
 // ---- RMS norm ----------------------------------------------------------------------------------
 // A workgroup a row.  Rows of up to kMaxHeld values stay in registers between the sum of squares and the norm
 // (C chunks of eight a thread); longer ones are read again.  One chunk a thread where 1024 threads hold the row:
-// 4096 x 8192 bf16 with the residual and the values 60 us (5.0 TB/s), two chunks of 512 threads 69.  16384 x 4096 108 us,
+// 4096 x 8192 bf16 with the residual and the values 60 us (5.0 TB/s), two chunks of 512 threads 69; without a residual
+// two chunks are the faster, 29.6 against 37 (683 x 8136 fp32: 10.5, 11.0).  16384 x 4096 108 us,
 // 5.6 TB/s (some of it from the last-level cache); with the weights loaded ahead of the sum 117, registers that
 // other rows could have used.  One row of 4096: 3.7 us, the chain of loads, sum, largest value and stores.
 constexpr int kNormThreads = 1024;
