@@ -7,7 +7,7 @@ import trellis_quantized_moe_expert_amd as q
 from f8_util import RULE, TYPE, dtype_of, norm_bound, packed, same, spread, within
 from gpu_util import say
 from oracle import f8
-from test_gpu_f8 import Experts, check_product, norm, product
+from test_gpu_f8 import Experts, check_norm, check_product, norm, product
 
 pytestmark = pytest.mark.gpu
 
@@ -172,3 +172,12 @@ def test_norm_into_scales_of_powers_of_two(rows, cols, kind):
     got = f8.TABLE[codes[:, :cols]] * s
     within(got, y, lim + np.maximum(2.0 ** -4 * (np.abs(y) + lim), s * 2.0 ** -10))
     assert not codes[:, cols:].any()
+
+
+@pytest.mark.parametrize("cols", [300, 40000])
+def test_norm_with_the_largest_eps(cols):
+    # the mean and eps together are past fp32's range
+    import torch
+    say(f"norm of {cols} columns with the largest eps")
+    x = (torch.rand(3, cols, generator=torch.Generator().manual_seed(6)) - 0.5).cuda() * (2.0 ** 63 / cols ** 0.5)
+    check_norm(x, "fp32", None, torch.ones(cols, device="cuda:0"), "fp32", float(np.finfo(np.float32).max))

@@ -199,8 +199,8 @@ __device__ inline NormFactor norm_factor(const F8NormParams& p, F squares) {
   NormFactor f;
   f.rstd64 = 0.0;
   f.rstd = 1.0f / sqrtf(sum / (float)p.cols + p.eps);
-  // Squares past fp32's range or next to its lower end (a NaN or an infinity comes here too and stays one)
-  f.wide = !(sum < 0x1p126f) || (sum < 0x1p-60f && sum != 0.0f) || (sum == 0.0f && p.eps < 0x1p-60f);
+  // Squares, or an eps, past fp32's range or next to its lower end (a NaN or an infinity comes here too and stays one)
+  f.wide = !(sum < 0x1p126f) || p.eps > 0x1p126f || (sum < 0x1p-60f && sum != 0.0f) || (sum == 0.0f && p.eps < 0x1p-60f);
   if (f.wide) f.rstd64 = 1.0 / sqrt(sum_of_all(squares(0.0), partial64) / p.cols + (double)p.eps);
   return f;
 }
