@@ -634,6 +634,8 @@ def _check_rows(fn: str, name: str, kind: str, obj, rows: int, cols: int, row_st
     if obj.numel() < last or not obj.is_contiguous():
         if obj.numel() == 0 or sum((n - 1) * st for n, st in zip(obj.shape, obj.stride())) < last - 1:
             _refuse(fn, name, "is smaller than its rows")
+        if cols > 1 and obj.shape[-1] > 1 and obj.stride(-1) != 1:
+            _refuse(fn, name, "must have a row's elements side by side")
 
 
 def qtip_mx_quantize(src, src_type, rows, cols, row_stride, scale_rule, codes, scales, values=None,
