@@ -1177,7 +1177,8 @@ constexpr int32_t kF8MostInputs = 1 << 23;
 qtip_status check_f8_inputs(const qtip_moe_plan_s* plan, int32_t pass) {
   const bool gu = pass == QTIP_F8_PASS_GATE_UP;
   if ((gu ? plan->d.hidden : plan->d.inter) < kF8MostInputs) return QTIP_OK;
-  return fail(QTIP_ERR_INVALID_ARG, gu ? "hidden must be below 2^23 for e4m3 experts" : "inter must be below 2^23 for e4m3 experts");
+  return fail(QTIP_ERR_INVALID_ARG, gu ? "hidden must be below 2^23 for e4m3 experts"
+                                       : "inter must be below 2^23 for e4m3 experts");
 }
 
 F8MatmulParams f8_pass_params(const qtip_moe_plan_s* plan, int32_t pass, const qtip_f8_weights* w,
